@@ -1,0 +1,88 @@
+/*
+ * muon.h -- C ABI of the matrix update operators of libembedding_wgrad.so
+ * (MI355X, gfx950): an update made from main_grad is orthogonalised by
+ * Newton-Schulz steps and applied to the weight.
+ *
+ * With U an update of `rows` x `cols`, X = U / (|U|_F + eps) (transposed where
+ * rows > cols), each of `steps` steps is
+ *
+ *     A = X X^T,   B = b A + c A A,   X <- a X + B X
+ *
+ * and the result is the last X, transposed back. Every singular value s of X
+ * goes to a s + b s^3 + c s^5 a step, so that with the usual coefficients
+ * (3.4445, -4.7750, 2.0315) five steps bring all but the smallest near 1.
+ * Sums and the state X are held in 32 bits, the norm in 64; the products
+ * read copies of X, A and B in 16-bit half precision. The result differs from
+ * the 64-bit one by about 0.05-0.1 % of its norm. A zero update gives zeros
+ * (eps keeps the division finite); a NaN or an infinity in an update makes
+ * that matrix's result NaN.
+ *
+ * The conventions of embedding_wgrad.h hold: device pointers owned by the
+ * caller, all work enqueued on `stream`, arguments checked on the host before
+ * anything is enqueued, no synchronisation, no allocation, kernels only (a
+ * call can be captured in a HIP graph). A batch of matrices of one size is one
+ * call. batch, rows or cols of zero: nothing is enqueued, EWG_OK. For given
+ * inputs every output bit is fixed.
+ *
+ * Strides are in elements: matrix i starts at i * batch_stride, its row r at
+ * r * row_stride, unit column stride; row_stride >= cols, and batch_stride
+ * at least one matrix's extent where batch > 1.
+ */
+#ifndef EWG_MUON_H
+#define EWG_MUON_H
+
+#include "embedding_wgrad.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Bounds: rows, cols <= EWG_MUON_MAX_SIDE, batch <= EWG_MUON_MAX_BATCH,
+ * 1 <= steps <= EWG_MUON_MAX_STEPS; EWG_UNSUPPORTED outside them. */
+#define EWG_MUON_MAX_SIDE 32768
+#define EWG_MUON_MAX_BATCH 65535
+#define EWG_MUON_MAX_STEPS 64
+
+/* Bytes of workspace both operators need for these sizes: about 10 bytes an
+ * element of the padded matrices and 4 for each of the Gram matrices' (host
+ * only; 0 for empty or out-of-range sizes). 256-byte aligned, needs no
+ * clearing, and must not be used by another call until this one has finished. */
+size_t orthogonalize_update_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+
+/*
+ * out = the orthogonalised update. update: EWG_BF16 or EWG_FP32; out: bf16,
+ * rounded once. out may be the update itself where that is bf16 with the same
+ * strides; otherwise they must not overlap.
+ */
+int orthogonalize_update(const void *update, void *out, int64_t batch, int64_t rows, int64_t cols,
+                         int64_t update_batch_stride, int64_t update_row_stride,
+                         int64_t out_batch_stride, int64_t out_row_stride, int update_dtype,
+                         int steps, float a, float b, float c, float eps, void *workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * One optimiser step from main_grad:
+ *
+ *     out_momentum = beta * momentum + main_grad
+ *     U            = main_grad + beta * out_momentum   (nesterov 1), or out_momentum (0)
+ *     out_weight   = weight * (1 - lr * weight_decay) - lr * scale * orthogonalised(U)
+ *
+ * weight, out_weight: weight_dtype (EWG_BF16 or EWG_FP32), main_grad:
+ * main_grad_dtype (EWG_BF16 or EWG_FP32), momentum: fp32. The arithmetic is in
+ * 32 bits with one rounding to the weight's type. out_weight is laid out as
+ * weight and may be weight itself; out_momentum likewise with momentum.
+ */
+int muon_step(const void *weight, void *out_weight, const void *main_grad, const float *momentum,
+              float *out_momentum, int64_t batch, int64_t rows, int64_t cols,
+              int64_t weight_batch_stride, int64_t weight_row_stride,
+              int64_t main_grad_batch_stride, int64_t main_grad_row_stride,
+              int64_t momentum_batch_stride, int64_t momentum_row_stride, int weight_dtype,
+              int main_grad_dtype, float lr, float beta, int nesterov, float weight_decay, float scale,
+              int steps, float a, float b, float c, float eps, void *workspace,
+              size_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* EWG_MUON_H */

@@ -1,0 +1,89 @@
+/*
+ * token_logprobs.h -- C ABI of the log-probability operators of
+ * libembedding_wgrad.so (MI355X, gfx950): the loss at the vocabulary end of a
+ * model, and the gradient that its backward pass starts from.
+ *
+ * For a row x of `vocab` logits and a temperature T, with y = x / T:
+ *
+ *     logsumexp = ln sum_j e^y_j            p_j = e^(y_j - logsumexp)
+ *     logprob   = y_target - logsumexp      entropy = -sum_j p_j ln p_j
+ *     alternatives: the top_k largest logits in order, equal ones by the lowest
+ *     index first, as (y - logsumexp, index)
+ *
+ * Sums are held in 32 bits. Masked logits -- -inf, and anything at or below
+ * -1e38, so that the types' lowest values count as masks -- have p = 0 and are
+ * no alternatives. The edges:
+ *   - a row with nothing left: logsumexp -inf, entropy 0, logprob -inf (0
+ *     without a target), no alternatives, gradient 0;
+ *   - a masked target: logprob -inf;
+ *   - a negative target names no token: logprob 0, and nothing of
+ *     grad_logprobs reaches that row;
+ *   - a target >= vocab: logprob NaN, and that row's gradient NaN;
+ *   - a NaN or +inf: NaN in all numbers of the row (logprob 0 without a
+ *     target), no alternatives;
+ *   - fewer than top_k alternatives: the rest hold -inf and index -1.
+ *
+ * The conventions of embedding_wgrad.h hold: device pointers owned by the
+ * caller, all work enqueued on `stream`, arguments checked on the host before
+ * anything is enqueued, no synchronisation, no allocation, kernels only (a
+ * call can be captured in a HIP graph). num_rows 0: nothing is enqueued,
+ * EWG_OK. For given inputs every output bit is fixed. Any element-aligned
+ * address and any row stride >= vocab is accepted.
+ */
+#ifndef EWG_TOKEN_LOGPROBS_H
+#define EWG_TOKEN_LOGPROBS_H
+
+#include "embedding_wgrad.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Bounds; EWG_UNSUPPORTED outside them. */
+#define EWG_MAX_TOP_LOGPROBS 32
+#define EWG_LOGPROBS_MAX_ROWS 1048576
+#define EWG_LOGPROBS_MAX_VOCAB 4194304
+
+/* Bytes of workspace token_logprobs needs (host only; 0 if out of range, or if
+ * it needs none: rows are split over workgroups, and the parts kept in the
+ * workspace, only where there are few of them). 256-byte aligned, needs no
+ * clearing, and must not be used by another call until this one has finished. */
+size_t token_logprobs_workspace_bytes(int64_t num_rows, int64_t vocab, int logits_dtype, int top_k);
+
+/*
+ * logits: num_rows x vocab (logits_dtype EWG_BF16 or EWG_FP32), row r at
+ * r * row_stride elements, unit column stride; targets: num_rows
+ * (targets_dtype EWG_INT32 or EWG_INT64). logprobs, entropy, logsumexp:
+ * num_rows floats; top_logprobs, top_ids: num_rows x top_k (may be NULL where
+ * top_k is 0). 0 <= top_k <= EWG_MAX_TOP_LOGPROBS, and top_k may exceed vocab.
+ * temperature within [1e-4, 1e4].
+ */
+int token_logprobs(const void *logits, const void *targets, int64_t num_rows, int64_t vocab,
+                   int64_t row_stride, int logits_dtype, int targets_dtype, float temperature, int top_k,
+                   float *logprobs, float *entropy, float *logsumexp, float *top_logprobs,
+                   int64_t *top_ids, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * grad_logits_j = (g ([j = target] - p_j) - h p_j (ln p_j + entropy)) / T
+ *
+ * for the gradients g of the logprobs and h of the entropy (num_rows floats
+ * each; NULL stands for zeros), with p_j = e^(y_j - logsumexp) from the
+ * logsumexp and entropy that token_logprobs returned for these logits. p
+ * inherits the rounding of logsumexp: its relative error is about |logsumexp|
+ * times 6e-8. grad_logits has the type of logits, rounded once, and may be
+ * logits itself (same stride); otherwise they must not overlap. entropy may
+ * be NULL where grad_entropy is. Rows of logits and grad_logits that share
+ * their offset in 16 bytes take the vector path.
+ */
+int token_logprobs_backward(const void *logits, const void *targets, const float *logsumexp,
+                            const float *entropy, const float *grad_logprobs,
+                            const float *grad_entropy, void *grad_logits, int64_t num_rows,
+                            int64_t vocab, int64_t row_stride, int64_t grad_row_stride,
+                            int logits_dtype, int targets_dtype, float temperature,
+                            hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* EWG_TOKEN_LOGPROBS_H */

@@ -50,6 +50,14 @@ EXPORTS = (
     "accumulate_embedding_wgrad_many_tokens",
     "accumulate_embedding_wgrad_many_tokens_timed",
     "ewg_status_string",
+    # include/token_logprobs.h
+    "token_logprobs_workspace_bytes",
+    "token_logprobs",
+    "token_logprobs_backward",
+    # include/muon.h
+    "orthogonalize_update_workspace_bytes",
+    "orthogonalize_update",
+    "muon_step",
     # include/embedding_wgrad_test.h (test-only)
     "ewg_test_accumulate_embedding_wgrad",
 )

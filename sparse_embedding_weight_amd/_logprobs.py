@@ -1,0 +1,184 @@
+"""Binding of include/token_logprobs.h: log probabilities of given tokens, with
+entropy and top alternatives, and their gradient. Argument marshalling only."""
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from ._binding import DTYPE_CODE, EWG_OK, EmbeddingWgradError, _stream_handle, lib
+
+MAX_TOP_LOGPROBS = 32             # EWG_MAX_TOP_LOGPROBS
+MAX_ROWS = 1048576                # EWG_LOGPROBS_MAX_ROWS
+MAX_VOCAB = 4194304               # EWG_LOGPROBS_MAX_VOCAB
+
+_i64, _int, _vp, _sz, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+
+lib.token_logprobs_workspace_bytes.argtypes = [_i64, _i64, _int, _int]
+lib.token_logprobs_workspace_bytes.restype = _sz
+lib.token_logprobs.argtypes = [_vp, _vp, _i64, _i64, _i64, _int, _int, _f32, _int] + [_vp] * 6 + [_sz, _vp]
+lib.token_logprobs.restype = _int
+lib.token_logprobs_backward.argtypes = [_vp] * 7 + [_i64] * 4 + [_int, _int, _f32, _vp]
+lib.token_logprobs_backward.restype = _int
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns. top_logprobs and top_ids are None for top_k = 0."""
+    logprobs: torch.Tensor
+    entropy: torch.Tensor
+    logsumexp: torch.Tensor
+    top_logprobs: Optional[torch.Tensor]
+    top_ids: Optional[torch.Tensor]
+
+
+def token_logprobs_workspace_bytes(num_rows: int, vocab: int, dtype: torch.dtype, top_k: int = 0) -> int:
+    """Bytes of workspace token_logprobs needs on the current device (0: none)."""
+    return lib.token_logprobs_workspace_bytes(num_rows, vocab, DTYPE_CODE.get(dtype, -1), top_k)
+
+
+# one workspace per (device, stream), grown on demand
+_WORKSPACES = {}
+
+
+def _workspace(need: int, device, stream: int, workspace):
+    if workspace is None:
+        key = (device.index, stream)
+        workspace = _WORKSPACES.get(key)
+        if workspace is None or workspace.numel() < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            _WORKSPACES[key] = workspace
+    elif workspace.dtype != torch.uint8 or workspace.device != device or workspace.numel() < need \
+            or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of >= {need} bytes on {device}")
+    return workspace
+
+
+def _check(what, logits, targets):
+    if not (isinstance(logits, torch.Tensor) and isinstance(targets, torch.Tensor)):
+        raise ValueError(f"{what}: logits and targets must be tensors")
+    if logits.device.type != "cuda" or targets.device != logits.device:
+        raise ValueError(f"{what}: logits and targets must be on one GPU")
+    if logits.dtype not in (torch.bfloat16, torch.float32) or targets.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"{what}: logits must be bfloat16 or float32, targets int32 or int64")
+    if logits.dim() < 1 or logits.shape[:-1] != targets.shape:
+        raise ValueError(f"{what}: logits must have the shape [*targets.shape, vocab]")
+    if not 1 <= logits.shape[-1] <= MAX_VOCAB or targets.numel() > MAX_ROWS:
+        raise ValueError(f"{what}: 1..{MAX_VOCAB} logits a row and at most {MAX_ROWS} rows")
+
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """[rows, vocab] with unit column stride; a view where the layout allows one."""
+    t2 = t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+    if t2.stride(1) != 1 and t2.shape[1] > 1:
+        t2 = t2.contiguous()
+    if t2.shape[0] > 1 and t2.stride(0) < t2.shape[1]:
+        t2 = t2.contiguous()
+    return t2
+
+
+def _temperature(what, temperature) -> float:
+    temperature = float(temperature)
+    if not 1e-4 <= temperature <= 1e4:
+        raise ValueError(f"{what}: temperature must lie within [1e-4, 1e4]")
+    return temperature
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top_k: int = 0, temperature: float = 1.0,
+                   workspace: torch.Tensor = None) -> TokenLogprobs:
+    """Log probability of each target under softmax(logits / temperature), with the
+    row's entropy and logsumexp and its top_k alternatives.
+
+    logits: [*, vocab], bfloat16 or float32; targets: [*], int32 or int64. A negative
+        target names no token (its logprob is 0), one >= vocab gives NaN.
+    top_k: 0..MAX_TOP_LOGPROBS alternatives a row, by logit, equal ones by the lowest
+        index first. -inf (and anything <= -1e38) is masked: no probability, no
+        alternative; where there are fewer than top_k the rest is (-inf, -1).
+    workspace: optional uint8 device tensor of >= token_logprobs_workspace_bytes(...);
+        by default a cached one per device and stream.
+    Returns float32 logprobs, entropy, logsumexp of targets' shape, float32
+    top_logprobs and int64 top_ids [*, top_k]. Enqueued on the current stream; no
+    sync. The edge cases are listed in include/token_logprobs.h."""
+    _check("token_logprobs", logits, targets)
+    temperature = _temperature("token_logprobs", temperature)
+    top_k = int(top_k)
+    if not 0 <= top_k <= MAX_TOP_LOGPROBS:
+        raise ValueError(f"token_logprobs: top_k must lie within 0..{MAX_TOP_LOGPROBS}")
+    device, shape, n, vocab = logits.device, targets.shape, targets.numel(), logits.shape[-1]
+    x, t = _rows(logits), targets.reshape(-1)
+    if not t.is_contiguous():
+        t = t.contiguous()
+    numbers = torch.empty((3, *shape), dtype=torch.float32, device=device)
+    top = torch.empty((*shape, top_k), dtype=torch.float32, device=device) if top_k else None
+    ids = torch.empty((*shape, top_k), dtype=torch.int64, device=device) if top_k else None
+    out = TokenLogprobs(numbers[0], numbers[1], numbers[2], top, ids)
+    if n == 0:
+        return out
+    code = DTYPE_CODE[logits.dtype]
+    with torch.cuda.device(device):
+        stream = _stream_handle(device)
+        need = lib.token_logprobs_workspace_bytes(n, vocab, code, top_k)
+        ws = _workspace(need, device, stream, workspace) if need or workspace is not None else None
+        at = numbers.data_ptr()
+        st = lib.token_logprobs(
+            x.data_ptr(), t.data_ptr(), n, vocab, x.stride(0), code, DTYPE_CODE[t.dtype], temperature,
+            top_k, at, at + 4 * n, at + 8 * n, top.data_ptr() if top_k else None,
+            ids.data_ptr() if top_k else None, ws.data_ptr() if ws is not None else None,
+            ws.numel() if ws is not None else 0, stream)
+    if st != EWG_OK:
+        raise EmbeddingWgradError(st, "token_logprobs")
+    return out
+
+
+def _per_row(name, t, shape, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or t.shape != shape:
+        raise ValueError(f"token_logprobs_backward: {name} must be a float32 tensor of targets' shape on {device}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, logsumexp: torch.Tensor,
+                            entropy: torch.Tensor = None, grad_logprobs: torch.Tensor = None,
+                            grad_entropy: torch.Tensor = None, temperature: float = 1.0,
+                            out: torch.Tensor = None) -> torch.Tensor:
+    """The gradient with respect to the logits, from the gradients of token_logprobs'
+    logprobs and entropy (float32 of targets' shape; None stands for zeros).
+
+    logsumexp, entropy: as token_logprobs returned them for these logits and this
+        temperature; entropy is needed with grad_entropy only.
+    out: optional tensor of logits' shape and type, rows of unit column stride; may be
+        logits itself, which is then overwritten.
+    Returns out. Enqueued on the current stream; no sync."""
+    _check("token_logprobs_backward", logits, targets)
+    temperature = _temperature("token_logprobs_backward", temperature)
+    device, shape, n, vocab = logits.device, targets.shape, targets.numel(), logits.shape[-1]
+    lse = _per_row("logsumexp", logsumexp, shape, device)
+    if grad_entropy is not None:
+        if entropy is None:
+            raise ValueError("token_logprobs_backward: grad_entropy needs entropy")
+        grad_entropy = _per_row("grad_entropy", grad_entropy, shape, device)
+        entropy = _per_row("entropy", entropy, shape, device)
+    if grad_logprobs is not None:
+        grad_logprobs = _per_row("grad_logprobs", grad_logprobs, shape, device)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=device)
+    elif out.dtype != logits.dtype or out.device != device or out.shape != logits.shape:
+        raise ValueError("token_logprobs_backward: out must have the shape, type and device of logits")
+    if n == 0:
+        return out
+    x = _rows(logits)
+    try:
+        o = out.view(n, vocab)
+    except RuntimeError:
+        o = None
+    if o is None or (o.stride(1) != 1 and vocab > 1) or (n > 1 and o.stride(0) < vocab):
+        raise ValueError("token_logprobs_backward: out must be viewable as [rows, vocab] with unit column stride")
+    t = targets.reshape(-1)
+    if not t.is_contiguous():
+        t = t.contiguous()
+    with torch.cuda.device(device):
+        st = lib.token_logprobs_backward(
+            x.data_ptr(), t.data_ptr(), lse.data_ptr(), entropy.data_ptr() if grad_entropy is not None else None,
+            grad_logprobs.data_ptr() if grad_logprobs is not None else None,
+            grad_entropy.data_ptr() if grad_entropy is not None else None, o.data_ptr(), n, vocab, x.stride(0),
+            o.stride(0), DTYPE_CODE[logits.dtype], DTYPE_CODE[t.dtype], temperature, _stream_handle(device))
+    if st != EWG_OK:
+        raise EmbeddingWgradError(st, "token_logprobs_backward")
+    return out

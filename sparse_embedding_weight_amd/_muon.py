@@ -1,0 +1,146 @@
+"""Binding of include/muon.h: orthogonalised updates and the optimiser step on
+main_grad built on them. Argument marshalling only."""
+import ctypes
+import math
+
+import torch
+
+from ._binding import DTYPE_CODE, EWG_OK, EmbeddingWgradError, _stream_handle, lib
+from ._logprobs import _workspace
+
+NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+MAX_SIDE = 32768                  # EWG_MUON_MAX_SIDE
+MAX_BATCH = 65535                 # EWG_MUON_MAX_BATCH
+MAX_STEPS = 64                    # EWG_MUON_MAX_STEPS
+
+_i64, _int, _vp, _sz, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+
+lib.orthogonalize_update_workspace_bytes.argtypes = [_i64] * 3
+lib.orthogonalize_update_workspace_bytes.restype = _sz
+lib.orthogonalize_update.argtypes = [_vp, _vp] + [_i64] * 7 + [_int, _int] + [_f32] * 4 + [_vp, _sz, _vp]
+lib.orthogonalize_update.restype = _int
+lib.muon_step.argtypes = ([_vp] * 5 + [_i64] * 9 + [_int, _int, _f32, _f32, _int, _f32, _f32, _int] + [_f32] * 4
+                          + [_vp, _sz, _vp])
+lib.muon_step.restype = _int
+
+
+def orthogonalize_update_workspace_bytes(batch: int, rows: int, cols: int) -> int:
+    """Bytes of workspace orthogonalize_update and muon_step need for these sizes."""
+    return lib.orthogonalize_update_workspace_bytes(batch, rows, cols)
+
+
+def _matrices(what, name, t):
+    """(batch, rows, cols, batch stride, row stride) of a matrix or a batch of them."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{what}: {name} must be a GPU tensor")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{what}: {name} must be a matrix or a batch of matrices")
+    batch = t.shape[0] if t.dim() == 3 else 1
+    rows, cols = t.shape[-2], t.shape[-1]
+    if batch > MAX_BATCH or rows > MAX_SIDE or cols > MAX_SIDE:
+        raise ValueError(f"{what}: at most {MAX_BATCH} matrices of at most {MAX_SIDE} x {MAX_SIDE}")
+    row_stride = t.stride(-2) if rows > 1 else max(cols, 1)
+    batch_stride = t.stride(0) if batch > 1 else rows * row_stride
+    if (t.stride(-1) != 1 and cols > 1) or row_stride < cols or \
+            (batch > 1 and batch_stride < (rows - 1) * row_stride + cols):
+        if t.numel():
+            raise ValueError(f"{what}: {name} must have unit column stride and rows that do not overlap")
+    return batch, rows, cols, batch_stride, row_stride
+
+
+def _newton_schulz_arguments(what, steps, coefficients, eps):
+    steps = int(steps)
+    if not 1 <= steps <= MAX_STEPS:
+        raise ValueError(f"{what}: steps must lie within 1..{MAX_STEPS}")
+    a, b, c = (float(v) for v in coefficients)
+    eps = float(eps)
+    if not all(math.isfinite(v) for v in (a, b, c, eps)) or eps < 0:
+        raise ValueError(f"{what}: coefficients must be finite and eps not negative")
+    return steps, a, b, c, eps
+
+
+def orthogonalize_update(update: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS,
+                         eps: float = 1e-7, out: torch.Tensor = None,
+                         workspace: torch.Tensor = None) -> torch.Tensor:
+    """The update with its singular values brought near 1 by Newton-Schulz steps
+    X <- a X + (b A + c A A) X, A = X X^T, from X = update / (|update|_F + eps).
+
+    update: [rows, cols] or [batch, rows, cols], bfloat16 or float32, unit column stride.
+    out: optional bfloat16 tensor of update's shape; may be update itself.
+    workspace: optional uint8 device tensor of >= orthogonalize_update_workspace_bytes(
+        batch, rows, cols); by default a cached one per device and stream.
+    Returns out, bfloat16. Enqueued on the current stream; no sync."""
+    what = "orthogonalize_update"
+    batch, rows, cols, bs, rs = _matrices(what, "update", update)
+    if update.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{what}: update must be bfloat16 or float32")
+    steps, a, b, c, eps = _newton_schulz_arguments(what, steps, coefficients, eps)
+    if out is None:
+        out = torch.empty(update.shape, dtype=torch.bfloat16, device=update.device)
+    elif out.dtype != torch.bfloat16 or out.device != update.device or out.shape != update.shape:
+        raise ValueError(f"{what}: out must be a bfloat16 tensor of update's shape and device")
+    _, _, _, obs, ors = _matrices(what, "out", out)
+    if update.numel() == 0:
+        return out
+    device = update.device
+    with torch.cuda.device(device):
+        stream = _stream_handle(device)
+        ws = _workspace(lib.orthogonalize_update_workspace_bytes(batch, rows, cols), device, stream, workspace)
+        st = lib.orthogonalize_update(update.data_ptr(), out.data_ptr(), batch, rows, cols, bs, rs, obs, ors,
+                                      DTYPE_CODE[update.dtype], steps, a, b, c, eps, ws.data_ptr(), ws.numel(),
+                                      stream)
+    if st != EWG_OK:
+        raise EmbeddingWgradError(st, what)
+    return out
+
+
+def muon_step(weight: torch.Tensor, main_grad: torch.Tensor, momentum: torch.Tensor, lr: float,
+              beta: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0, scale: float = None,
+              steps: int = 5, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps: float = 1e-7,
+              out_weight: torch.Tensor = None, out_momentum: torch.Tensor = None,
+              workspace: torch.Tensor = None) -> None:
+    """One optimiser step of a matrix (or a batch of them) from its main_grad:
+
+        momentum <- beta momentum + main_grad
+        U         = main_grad + beta momentum (nesterov), or momentum
+        weight   <- weight (1 - lr weight_decay) - lr scale orthogonalize_update(U)
+
+    weight, main_grad: bfloat16 or float32; momentum: float32; all of one shape, unit
+        column stride. scale defaults to sqrt(max(1, rows / cols)).
+    out_weight, out_momentum: where the new values go, laid out as weight and momentum
+        are; by default weight and momentum are updated in place.
+    workspace: as for orthogonalize_update. Enqueued on the current stream; no sync."""
+    what = "muon_step"
+    batch, rows, cols, wbs, wrs = _matrices(what, "weight", weight)
+    device = weight.device
+    g = _matrices(what, "main_grad", main_grad)
+    m = _matrices(what, "momentum", momentum)
+    if main_grad.shape != weight.shape or momentum.shape != weight.shape:
+        raise ValueError(f"{what}: weight, main_grad and momentum must have one shape")
+    if main_grad.device != device or momentum.device != device:
+        raise ValueError(f"{what}: weight, main_grad and momentum must be on one GPU")
+    if weight.dtype not in (torch.bfloat16, torch.float32) or main_grad.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{what}: weight and main_grad must be bfloat16 or float32")
+    if momentum.dtype != torch.float32:
+        raise ValueError(f"{what}: momentum must be float32")
+    steps, a, b, c, eps = _newton_schulz_arguments(what, steps, coefficients, eps)
+    for name, t, like, layout in (("out_weight", out_weight, weight, (batch, rows, cols, wbs, wrs)),
+                                  ("out_momentum", out_momentum, momentum, m)):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != like.dtype or t.device != device
+                              or t.shape != like.shape or _matrices(what, name, t) != layout):
+            raise ValueError(f"{what}: {name} must have the type, shape, strides and device of {name[4:]}")
+    out_weight = weight if out_weight is None else out_weight
+    out_momentum = momentum if out_momentum is None else out_momentum
+    if weight.numel() == 0:
+        return
+    scale = math.sqrt(max(1.0, rows / cols)) if scale is None else float(scale)
+    with torch.cuda.device(device):
+        stream = _stream_handle(device)
+        ws = _workspace(lib.orthogonalize_update_workspace_bytes(batch, rows, cols), device, stream, workspace)
+        st = lib.muon_step(weight.data_ptr(), out_weight.data_ptr(), main_grad.data_ptr(), momentum.data_ptr(),
+                           out_momentum.data_ptr(), batch, rows, cols, wbs, wrs, g[3], g[4], m[3], m[4],
+                           DTYPE_CODE[weight.dtype], DTYPE_CODE[main_grad.dtype], float(lr), float(beta),
+                           1 if nesterov else 0, float(weight_decay), scale, steps, a, b, c, eps, ws.data_ptr(),
+                           ws.numel(), stream)
+    if st != EWG_OK:
+        raise EmbeddingWgradError(st, what)

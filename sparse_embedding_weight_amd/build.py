@@ -12,7 +12,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIBRARY = os.path.join(HERE, "libembedding_wgrad.so")
-SOURCES = ["api.hip", "sort_tokens.hip", "accumulate.hip", "many_tokens.hip"]
+SOURCES = ["api.hip", "sort_tokens.hip", "accumulate.hip", "many_tokens.hip", "token_logprobs.hip",
+           "newton_schulz.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

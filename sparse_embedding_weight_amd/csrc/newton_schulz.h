@@ -1,0 +1,44 @@
+// Shapes, workspace layout and kernel parameters of the Newton-Schulz
+// operators (newton_schulz.hip). Not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "ewg_internal.h"
+
+namespace ewg {
+
+// The iterated matrix X is the update with its shorter side first: k x len,
+// transposed when the update has more rows than columns. Both sides are
+// padded with zeros to whole tiles, so no product checks a bound; a zero row
+// or column stays zero through every step.
+struct NsShape {
+    int batch;
+    int rows, cols;        // the update as the caller holds it
+    int tall;              // rows > cols: X is its transpose
+    int k, len;            // X: min and max of rows, cols
+    int kp, lp;            // padded
+    int tile;              // tile side of the products
+};
+
+// Byte offsets in the workspace (one matrix after another inside each part).
+struct NsLayout {
+    size_t partials;       // double [batch][kNsMaxPartials], sums of squares
+    size_t x;              // float  [batch][kp][lp], the state
+    size_t xh;             // half   [batch][kp][lp], scaled copy for X X^T
+    size_t xt0, xt1;       // half   [batch][lp][kp], its transpose for B X, two in turn
+    size_t a, b;           // half   [batch][kp][kp], the Gram matrix and the polynomial, zero diagonals
+    size_t diag_a, diag_b; // float  [batch][kp], their diagonals
+    size_t total;
+};
+
+constexpr int kNsMaxPartials = 256;
+constexpr int64_t kNsMaxSide = 32768;     // keeps every in-matrix index of a tile row in 32 bits
+constexpr int64_t kNsMaxBatch = 65535;    // grid.y
+
+NsShape ns_shape(int64_t batch, int64_t rows, int64_t cols);
+NsLayout ns_layout(const NsShape &s);
+
+}  // namespace ewg
