@@ -12,8 +12,8 @@ namespace ewg {
 
 // The iterated matrix X is the update with its shorter side first: k x len,
 // transposed when the update has more rows than columns. Both sides are
-// padded with zeros to whole tiles, so no product checks a bound; a zero row
-// or column stays zero through every step.
+// padded with zeros to multiples of 64; a zero row or column stays zero through
+// every step.
 struct NsShape {
     int batch;
     int rows, cols;        // the update as the caller holds it
@@ -34,7 +34,7 @@ struct NsLayout {
     size_t total;
 };
 
-constexpr int kNsMaxPartials = 256;
+constexpr int kNsMaxPartials = 2048;
 constexpr int64_t kNsMaxSide = 32768;     // keeps every in-matrix index of a tile row in 32 bits
 constexpr int64_t kNsMaxBatch = 65535;    // grid.y
 

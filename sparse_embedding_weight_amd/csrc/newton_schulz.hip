@@ -27,6 +27,8 @@
 
 #include <hip/hip_fp16.h>
 
+#include <type_traits>
+
 #include "ewg_device.h"
 #include "muon.h"
 
@@ -70,30 +72,75 @@ __device__ __forceinline__ float load_u(const NsSource &s, int b, int r, int c) 
 }
 
 // Sums u^2 in 64 bits (squares of 1e-25 or 1e25 neither vanish nor overflow),
-// a fixed share of the rows and a fixed order for every workgroup. One pass
-// over main_grad and momentum; bound by HBM.
+// a fixed share and a fixed order for every workgroup. One pass over main_grad
+// and momentum, bound by HBM: four elements of a row at a time, four of those
+// in flight a lane; a lane's next place is its last plus a constant number of
+// rows and columns, so that no index is divided in the loop.
 template <class G, bool MOM>
-__global__ __launch_bounds__(256) void ns_norm_kernel(NsSource s, int rows, int cols,
+__global__ __launch_bounds__(256) void ns_norm_kernel(NsSource s, int rows, int cols, int vector,
                                                       double *__restrict__ partials) {
-    const int b = blockIdx.y, parts = gridDim.x;
+    const int b = blockIdx.y;
     double sum = 0.0;
-    const int64_t total = (int64_t)rows * cols;
-    const int64_t share = ((total + parts - 1) / parts + 255) / 256 * 256;
-    const int64_t first = (int64_t)blockIdx.x * share;
-    const int64_t last = first + share < total ? first + share : total;
-    for (int64_t i = first + threadIdx.x; i < last; i += 256) {
-        const int r = (int)(i / cols), c = (int)(i - (int64_t)r * cols);
-        float u;
+    const int width = vector ? 4 : 1;
+    const int across = cols / width;             // groups a row
+    const int stride = gridDim.x * 256;
+    const int dr = stride / across, dc = stride - dr * across;
+    const int first = blockIdx.x * 256 + threadIdx.x;
+    int r = first / across, c = first - r * across;
+    auto one = [&](float g, float m, float &m_new) {
+        float u = g;
         if constexpr (MOM) {
-            const float g = load_g<G>(s, b, r, c);
-            const int64_t at = b * s.m_batch + r * s.m_row + c;
-            const float m = __builtin_fmaf(s.beta, s.m[at], g);
-            s.m_out[at] = m;
-            u = s.nesterov ? __builtin_fmaf(s.beta, m, g) : m;
-        } else {
-            u = load_g<G>(s, b, r, c);
+            m_new = __builtin_fmaf(s.beta, m, g);
+            u = s.nesterov ? __builtin_fmaf(s.beta, m_new, g) : m_new;
         }
         sum += (double)u * (double)u;
+    };
+    const typename G::T *g0 = static_cast<const typename G::T *>(s.g) + b * s.g_batch;
+    auto advance = [&]() {
+        r += dr;
+        c += dc;
+        if (c >= across) {
+            c -= across;
+            ++r;
+        }
+    };
+    if (vector) {
+        while (r < rows) {
+            typename G::T g[4][4];
+            float m[4][4];
+            int64_t at[4];
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                at[i] = -1;
+                if (r < rows) {
+                    load_vec<typename G::T, 4>(g0 + r * s.g_row + c * 4, g[i]);
+                    if constexpr (MOM) {
+                        at[i] = b * s.m_batch + r * s.m_row + c * 4;
+                        load_vec<float, 4>(s.m + at[i], m[i]);
+                    }
+                    n = i + 1;
+                    advance();
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i < n) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) one(G::widen(g[i][e]), m[i][e], m[i][e]);
+                    if constexpr (MOM) store_vec<float, 4>(s.m_out + at[i], m[i]);
+                }
+            }
+        }
+    } else {
+        while (r < rows) {
+            const int64_t at = b * s.m_batch + r * s.m_row + c;
+            float m = 0.0f;
+            if constexpr (MOM) m = s.m[at];
+            one(G::widen(g0[r * s.g_row + c]), m, m);
+            if constexpr (MOM) s.m_out[at] = m;
+            advance();
+        }
     }
     __shared__ double part[256];
     part[threadIdx.x] = sum;
@@ -117,7 +164,9 @@ __global__ __launch_bounds__(256) void ns_layout_kernel(NsSource s, NsShape sh, 
     __shared__ float t[64][65];
     __shared__ double part[256];
     const int b = blockIdx.z, tid = threadIdx.x;
-    part[tid] = tid < parts ? partials[(int64_t)b * kNsMaxPartials + tid] : 0.0;
+    double share = 0.0;
+    for (int i = tid; i < parts; i += 256) share += partials[(int64_t)b * kNsMaxPartials + i];
+    part[tid] = share;
     __syncthreads();
     for (int n = 128; n > 0; n >>= 1) {
         if (tid < n) part[tid] += part[tid + n];
@@ -156,13 +205,14 @@ struct NsSink {
     int64_t out_batch, out_row;
     const void *weight;        // old weight (same layout as out), or null
     float keep, take;          // weight * keep - take * X
+    bool vector;               // groups of four elements of out and weight are aligned
 };
 
 struct NsProduct {
     const _Float16 *p, *q;     // C = P Q^T, both [rows][depth]
     int64_t p_batch, q_batch;
     int depth;                 // padded, a multiple of 64
-    int tiles_p, tiles_q;
+    int tiles_p, tiles_q;      // of one matrix
     // epilogue
     float factor;              // on the 32-bit sums
     const _Float16 *gram;      // for B: A without its diagonal
@@ -177,38 +227,136 @@ struct NsProduct {
 
 enum NsEpilogue { kGram, kPoly, kState, kLast };
 
-// XOR swizzle of the 16-byte pieces of a 128-byte tile row: 32 lanes reading
-// one piece column of 32 rows then touch every bank group equally.
-__device__ __forceinline__ int swizzled(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
-
-template <class S, bool WEIGHT>
-__device__ __forceinline__ void sink_one(const NsSink &k, int64_t at, float v) {
-    typename S::T *out = static_cast<typename S::T *>(k.out);
-    if constexpr (WEIGHT) {
-        const float w = S::widen(static_cast<const typename S::T *>(k.weight)[at]);
-        v = __builtin_fmaf(-k.take, v, w * k.keep);
-    }
-    out[at] = S::narrow(v);
+// Lane r of four holds o[e] = M[r][e]; afterwards it holds M[e][r], e = 0..3:
+// four rows' values of one column side by side, for one 8-byte store where the
+// transposed matrix is written instead of four 2-byte ones.
+__device__ __forceinline__ half4 transpose_quad(half4 o) {
+    uint32_t d0, d1;
+    __builtin_memcpy(&d0, &o, 4);
+    __builtin_memcpy(&d1, reinterpret_cast<const char *>(&o) + 4, 4);
+    const bool odd = threadIdx.x & 1, upper = threadIdx.x & 2;
+    const uint32_t t0 = __builtin_amdgcn_mov_dpp(d0, 0xb1, 0xf, 0xf, true);      // lanes 1 0 3 2
+    const uint32_t t1 = __builtin_amdgcn_mov_dpp(d1, 0xb1, 0xf, 0xf, true);
+    const uint32_t pick = odd ? 0x03020706u : 0x05040100u;                       // bytes 0-3: second operand, 4-7: first
+    d0 = __builtin_amdgcn_perm(t0, d0, pick);
+    d1 = __builtin_amdgcn_perm(t1, d1, pick);
+    const uint32_t sent = upper ? d0 : d1;
+    const uint32_t got = __builtin_amdgcn_mov_dpp(sent, 0x4e, 0xf, 0xf, true);   // lanes 2 3 0 1
+    const uint32_t lo = upper ? got : d0, hi = upper ? d1 : got;
+    half4 r;
+    __builtin_memcpy(&r, &lo, 4);
+    __builtin_memcpy(reinterpret_cast<char *>(&r) + 4, &hi, 4);
+    return r;
 }
 
-// One tile of C = P Q^T. Tiles of 64 halves of depth go through LDS twice
-// buffered, written by direct-to-LDS loads; each of the WP x WQ waves keeps
-// (TP/WP) x (TQ/WQ) of C in registers as 32x32 blocks. The matrix
-// instruction takes Q as its first operand: a lane then holds four
-// consecutive columns of one row of C.
-template <int TP, int TQ, int WP, int WQ, int EPI, class S, bool WEIGHT>
-__global__ __launch_bounds__(WP *WQ * 64) void ns_product_kernel(NsProduct a, NsSink sink) {
-    constexpr int WAVES = WP * WQ;
-    constexpr int FP = TP / WP / 32, FQ = TQ / WQ / 32;
-    constexpr int PIECES = (TP + TQ) / 8;            // 1 KiB wave loads a tile
-    static_assert(PIECES % WAVES == 0 && TP % 8 == 0, "whole loads");
-    constexpr int LOADS = PIECES / WAVES;
-    constexpr int BYTES = (TP + TQ) * 128;
+// The same for 32-bit values.
+__device__ __forceinline__ void transpose_quad(float (&v)[4]) {
+    const bool odd = threadIdx.x & 1, upper = threadIdx.x & 2;
+    auto from = [](float x, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    using Swap1 = std::integral_constant<int, 0xb1>;
+    using Swap2 = std::integral_constant<int, 0x4e>;
+    const float a = from(odd ? v[0] : v[1], Swap1()), b = from(odd ? v[2] : v[3], Swap1());
+    const float w[4] = {odd ? a : v[0], odd ? v[1] : a, odd ? b : v[2], odd ? v[3] : b};
+    const float c = from(upper ? w[0] : w[2], Swap2()), d = from(upper ? w[1] : w[3], Swap2());
+    v[0] = upper ? c : w[0];
+    v[1] = upper ? d : w[1];
+    v[2] = upper ? w[2] : c;
+    v[3] = upper ? w[3] : d;
+}
+
+// Four of the last X's values, (row, col..col+3) of it, to the caller's output or
+// into the weight; every lane of the wave takes part.
+template <class S, bool WEIGHT>
+__device__ __forceinline__ void sink_four(const NsSink &k, const NsShape &sh, int batch, int row, int col, float (&v)[4]) {
+    int r = row, c = col;
+    if (sh.tall) {
+        transpose_quad(v);
+        r = col + (threadIdx.x & 3);
+        c = row & ~3;
+    }
+    if (r >= sh.rows || c >= sh.cols) return;
+    using T = typename S::T;
+    const int64_t at = batch * k.out_batch + r * k.out_row + c;
+    T *out = static_cast<T *>(k.out) + at;
+    const T *weight = static_cast<const T *>(k.weight) + at;
+    if (k.vector && c + 4 <= sh.cols) {
+        T o[4];
+        if constexpr (WEIGHT) {
+            T w[4];
+            load_vec<T, 4>(weight, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(-k.take, v[e], S::widen(w[e]) * k.keep);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = S::narrow(v[e]);
+        store_vec<T, 4>(out, o);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < sh.cols) {
+                if constexpr (WEIGHT) v[e] = __builtin_fmaf(-k.take, v[e], S::widen(weight[e]) * k.keep);
+                out[e] = S::narrow(v[e]);
+            }
+    }
+}
+
+// LDS tile: rows of 32 halves, 64 bytes, in four 16-byte pieces; piece c of row
+// r lies at place c ^ (r / 4 % 4), so that sixteen lanes reading one piece of
+// sixteen rows touch each of the 64 banks once (r / 2 % 4, which spreads eight
+// rows over 32 banks, cost four more clocks a read by the conflict counter).
+__device__ __forceinline__ int swizzled(int row, int piece) { return row * 64 + ((piece ^ ((row >> 2) & 3)) << 4); }
+
+typedef int int4v __attribute__((ext_vector_type(4)));
+
+// a value that is the same in every lane, as a scalar
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A wave's direct-to-LDS load: 64 lanes x 16 bytes from base + voffset + soffset
+// to the LDS bytes [lds, lds + 1024). Written as an instruction because the
+// compiler, which cannot tell the stages of the ring apart, would wait for all
+// loads in flight before every LDS read. It has no output register; what has
+// arrived is settled by wait_loads and a barrier before a stage is read.
+__device__ __forceinline__ void load_to_lds(int4v base, int voffset, int soffset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(lds), "v"(voffset), "s"(base), "s"(soffset) : "memory");
+}
+
+// Waits until at most N of this wave's loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+
+constexpr int kDepth = 32;       // of a stage
+
+// Stages of the LDS ring: 128 KiB for a 256 x 256 tile, 64 for a 128 x 128 one,
+// so that two workgroups of those share a compute unit (a ring of eight and one
+// workgroup: no faster alone, and slower where there are many tiles).
+constexpr int kStages = 4;
+
+// One tile of C = P Q^T, 64 FP x 64 FQ, by four waves of 32 FP x 32 FQ each, kept
+// in registers as 32x32 blocks. P and Q go through a ring of LDS stages of
+// 32 halves of depth, loaded a ring less one ahead; a wave reads the operands of
+// the next 16 of depth from LDS while the matrix instructions of the present 16
+// run, so that one wave a SIMD keeps the matrix unit fed. 128 x 128 a wave
+// rather than 128 x 64 because the LDS is the next bound: a stage's reads and
+// writes take 1536 of its 2048 clocks' worth of matrix work per 64 of depth
+// instead of all 2048. The matrix instruction takes Q as its first operand: a
+// lane then holds four consecutive columns of one row of C.
+template <int FP, int FQ, int EPI, class S, bool WEIGHT>
+__global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sink) {
+    constexpr int TP = 64 * FP, TQ = 64 * FQ;
+    constexpr int LOADS = (TP + TQ) / 64;            // 1 KiB (16 rows) loads of a wave and stage
+    constexpr int BYTES = (TP + TQ) * 64;
     constexpr bool SYM = EPI == kGram || EPI == kPoly;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * BYTES];
+    constexpr int RING = kStages;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[RING * BYTES];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int stages = a.depth / kDepth;
     const int batch = blockIdx.y;
     int ti, tj;
     if constexpr (SYM) {
@@ -217,88 +365,153 @@ __global__ __launch_bounds__(WP *WQ * 64) void ns_product_kernel(NsProduct a, Ns
         ti = (int)((sqrtf(8.0f * (float)n + 1.0f) - 1.0f) * 0.5f);
         while ((ti + 1) * (ti + 2) / 2 <= n) ++ti;
         while (ti * (ti + 1) / 2 > n) --ti;
+        ti = uniform(ti);
         tj = n - ti * (ti + 1) / 2;
     } else {
-        ti = blockIdx.x % a.tiles_p;
-        tj = blockIdx.x / a.tiles_p;
+        tj = uniform((int)blockIdx.x / a.tiles_p);
+        ti = (int)blockIdx.x - tj * a.tiles_p;
     }
-    const _Float16 *p = a.p + batch * a.p_batch + (int64_t)ti * TP * a.depth;
-    const _Float16 *q = a.q + batch * a.q_batch + (int64_t)tj * TQ * a.depth;
 
-    // lane l of a load brings row l/8 of eight, piece (l%8) ^ (l/8) of it
-    const int row8 = lane >> 3, piece = (lane & 7) ^ row8;
-    const _Float16 *from[LOADS];
+    // Buffer descriptors of the tile's rows of P and Q: base, bytes, raw format. A
+    // tile is at most 256 rows of 64 KiB, so offsets fit; rows of the last tile that
+    // lie past the matrix are past the descriptor's bytes, and read as zeros.
+    auto descriptor = [&](const _Float16 *p, int rows) {
+        const uint64_t at = reinterpret_cast<uint64_t>(p);
+        int4v d;
+        d[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+        d[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32) & 0xffff);
+        d[2] = rows * a.depth * 2;
+        d[3] = 0x00020000;
+        return d;
+    };
+    const int rows_p = a.sh.kp - ti * TP, rows_q = (SYM ? a.sh.kp : a.sh.lp) - tj * TQ;
+    const int4v dp = descriptor(a.p + batch * a.p_batch + (int64_t)ti * TP * a.depth, rows_p < TP ? rows_p : TP);
+    const int4v dq = descriptor(a.q + batch * a.q_batch + (int64_t)tj * TQ * a.depth, rows_q < TQ ? rows_q : TQ);
+    // Lane l of a load brings piece (l % 4) ^ (l / 16) of row l / 4 of sixteen.
+    // Load i of wave w holds rows 16 (4 i + w): all of a load lie in P or in Q.
+    const int row16 = lane >> 2, piece = (lane & 3) ^ (lane >> 4);
+    const int voffset = (wave * 16 + row16) * a.depth * 2 + piece * 16;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + wave * 1024;
+    // loads [first, last) of a stage
+    auto stage = [&](int t, int first, int last) {
+        // past the end the last stage is loaded again, so that the count of loads in flight stays the same
+        const int from = (t < stages ? t : stages - 1) * kDepth * 2;
+        const uint32_t to = lds0 + (uint32_t)(t & (RING - 1)) * BYTES;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        const int row = (i * WAVES + wave) * 8;
-        from[i] = (row < TP ? p + (int64_t)(row + row8) * a.depth : q + (int64_t)(row - TP + row8) * a.depth) + piece * 8;
-    }
-    auto stage = [&](int buffer, int kt) {
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void *)(from[i] + kt * 64),
-                (__attribute__((address_space(3))) void *)(lds + buffer * BYTES + (i * WAVES + wave) * 1024), 16, 0, 0);
+        for (int i = first; i < last; ++i) {
+            const bool in_p = i < FP;
+            load_to_lds(in_p ? dp : dq, voffset, from + (in_p ? i : i - FP) * 64 * a.depth * 2, to + i * 4096);
+        }
     };
 
-    const int wp = wave % WP, wq = wave / WP;
+    const int wp = wave & 1, wq = wave >> 1;
     const int r32 = lane & 31, h = lane >> 5;
+    // LDS places of the wave's operands, for the two halves of a stage's depth
+    int p_at[2], q_at[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        p_at[s] = swizzled(wp * FP * 32 + r32, s * 2 + h);
+        q_at[s] = TP * 64 + swizzled(wq * FQ * 32 + r32, s * 2 + h);
+    }
+    half8 pf[2][FP], qf[2][FQ];
     float16v acc[FP][FQ] = {};
-    const int steps = a.depth / 64;
-    stage(0, 0);
-    for (int kt = 0; kt < steps; ++kt) {
-        // this tile has arrived for every wave, and every wave has read the one before
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __syncthreads();
-        const uint8_t *tile = lds + (kt & 1) * BYTES;
-        half8 pf[4][FP], qf[4][FQ];
+    // Half a stage: the matrix instructions of depth half s, block row by block row;
+    // between the rows the reads of the half that comes next and a share of the
+    // loads of a stage to come go out. All eight loads of a wave at once would hold
+    // it up behind the address unit (16 clocks a load) with the matrix unit idle.
+    auto read = [&](const uint8_t *tile, int s, int i) {
+        pf[s][i] = *reinterpret_cast<const half8 *>(tile + p_at[s] + i * 2048);
+        qf[s][i] = *reinterpret_cast<const half8 *>(tile + q_at[s] + i * 2048);
+    };
+    auto half_stage = [&](int s, int next, int load, int first) {
+        const uint8_t *tile = lds + (next & (RING - 1)) * BYTES;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-#pragma unroll
-            for (int i = 0; i < FP; ++i)
-                pf[s][i] = *reinterpret_cast<const half8 *>(tile + swizzled(wp * FP * 32 + i * 32 + r32, s * 2 + h));
+        for (int i = 0; i < FP; ++i) {
+            read(tile, 1 - s, i);
+            stage(load, first + i * LOADS / 2 / FP, first + (i + 1) * LOADS / 2 / FP);
 #pragma unroll
             for (int j = 0; j < FQ; ++j)
-                qf[s][j] = *reinterpret_cast<const half8 *>(tile + TP * 128 + swizzled(wq * FQ * 32 + j * 32 + r32, s * 2 + h));
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[s][j], pf[s][i], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (kt + 1 < steps) stage((kt + 1) & 1, kt + 1);
+    };
+    static_assert(FP == FQ && LOADS % 2 == 0, "rows of blocks share out reads and loads evenly");
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+    for (int t = 0; t < RING - 2; ++t) stage(t, 0, LOADS);
+    stage(RING - 2, 0, LOADS / 2);
+    wait_loads<(RING - 3) * LOADS + LOADS / 2>();
+    __builtin_amdgcn_s_barrier();
 #pragma unroll
-            for (int i = 0; i < FP; ++i)
-#pragma unroll
-                for (int j = 0; j < FQ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[s][j], pf[s][i], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < FP; ++i) read(lds, 0, i);
+    for (int t = 0; t < stages; ++t) {
+        half_stage(0, t, t + RING - 2, LOADS / 2);
+        // stage t + 1 is there for every wave, and every wave has read stage t - 1
+        wait_loads<(RING - 3) * LOADS>();
+        __builtin_amdgcn_s_barrier();
+        half_stage(1, t + 1, t + RING - 1, 0);
     }
+    wait_loads<0>();
 
     const int kp = a.sh.kp, lp = a.sh.lp;
     float *diag_a = a.diag_a + (int64_t)batch * kp, *diag_b = a.diag_b + (int64_t)batch * kp;
+    const int64_t base = (int64_t)batch * kp * (SYM ? kp : lp);
+    const int width = SYM ? kp : lp;
+    // What the results are made of (A's halves for B, the state for X): the
+    // loads of one row of blocks go out before the row before is worked on.
+    // Blocks past the matrix (its sides are multiples of 64) are left out.
+    using In = typename std::conditional<EPI == kPoly, half4, float4>::type;
+    constexpr bool READS = EPI != kGram;
+    In in[2][FQ][4];
+    auto row_of = [&](int i) { return ti * TP + (wp * FP + i) * 32 + r32; };
+    auto block_in = [&](int i, int j) { return ti * TP + (wp * FP + i) * 32 < kp && tj * TQ + (wq * FQ + j) * 32 < width; };
+    auto col_of = [&](int j, int g) { return tj * TQ + (wq * FQ + j) * 32 + g * 8 + h * 4; };
+    auto fetch = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < FQ; ++j)
+            if (block_in(i, j)) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int64_t at = base + (int64_t)row_of(i) * width + col_of(j, g);
+                    if constexpr (EPI == kPoly) in[i & 1][j][g] = *reinterpret_cast<const half4 *>(a.gram + at);
+                    if constexpr (EPI == kState || EPI == kLast) in[i & 1][j][g] = *reinterpret_cast<const float4 *>(a.x + at);
+                }
+            }
+    };
+    if constexpr (READS) fetch(0);
 #pragma unroll
     for (int i = 0; i < FP; ++i) {
-        const int row = ti * TP + (wp * FP + i) * 32 + r32;
+        // one row of blocks after another: more loads at the front would spill
+        asm volatile("" ::: "memory");
+        if constexpr (READS)
+            if (i + 1 < FP) fetch(i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        const int row = row_of(i);
         // a + e for X's row; A's diagonal for B's
         float of_row = 0.0f;
-        if constexpr (EPI == kPoly) of_row = diag_a[row];
-        if constexpr (EPI == kState || EPI == kLast) of_row = a.a_coef + diag_b[row];
+        if (row < kp) {
+            if constexpr (EPI == kPoly) of_row = diag_a[row];
+            if constexpr (EPI == kState || EPI == kLast) of_row = a.a_coef + diag_b[row];
+        }
 #pragma unroll
         for (int j = 0; j < FQ; ++j) {
+            if (!block_in(i, j)) continue;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int col = tj * TQ + (wq * FQ + j) * 32 + g * 8 + h * 4;
+                const int col = col_of(j, g);
+                const int64_t at = base + (int64_t)row * width + col;
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = acc[i][j][g * 4 + e] * a.factor;
                 if constexpr (SYM) {
-                    _Float16 *out = a.out + (int64_t)batch * kp * kp;
                     if constexpr (EPI == kPoly) {
-                        const half4 gram = *reinterpret_cast<const half4 *>(a.gram + (int64_t)batch * kp * kp + (int64_t)row * kp + col);
                         const float4 of_col = *reinterpret_cast<const float4 *>(diag_a + col);
                         const float dc[4] = {of_col.x, of_col.y, of_col.z, of_col.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             if (row == col + e)
                                 diag_b[row] = (v[e] + of_row * __builtin_fmaf(of_row, a.c_coef / kGramScale, a.b_coef)) / kGramScale;
-                            v[e] = __builtin_fmaf(__builtin_fmaf(of_row + dc[e], a.c_coef / kGramScale, a.b_coef), (float)gram[e], v[e]);
+                            v[e] = __builtin_fmaf(__builtin_fmaf(of_row + dc[e], a.c_coef / kGramScale, a.b_coef),
+                                                  (float)in[i & 1][j][g][e], v[e]);
                         }
                     } else {
 #pragma unroll
@@ -308,15 +521,11 @@ __global__ __launch_bounds__(WP *WQ * 64) void ns_product_kernel(NsProduct a, Ns
                     half4 o;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[e] = row == col + e ? (_Float16)0.0f : (_Float16)v[e];
-                    *reinterpret_cast<half4 *>(out + (int64_t)row * kp + col) = o;
-                    if (ti != tj) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) out[(int64_t)(col + e) * kp + row] = o[e];
-                    }
+                    *reinterpret_cast<half4 *>(a.out + at) = o;
+                    if (ti != tj)
+                        *reinterpret_cast<half4 *>(a.out + base + (int64_t)(col + (lane & 3)) * kp + (row & ~3)) = transpose_quad(o);
                 } else {
-                    const int64_t base = (int64_t)batch * kp * lp;
-                    const int64_t at = base + (int64_t)row * lp + col;
-                    const float4 old = *reinterpret_cast<const float4 *>(a.x + at);
+                    const In old = in[i & 1][j][g];
                     v[0] = __builtin_fmaf(of_row, old.x, v[0]);
                     v[1] = __builtin_fmaf(of_row, old.y, v[1]);
                     v[2] = __builtin_fmaf(of_row, old.z, v[2]);
@@ -327,16 +536,9 @@ __global__ __launch_bounds__(WP *WQ * 64) void ns_product_kernel(NsProduct a, Ns
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[e] = (_Float16)(v[e] * a.x_scale);
                         *reinterpret_cast<half4 *>(a.out + at) = o;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) a.out_t[base + (int64_t)(col + e) * kp + row] = o[e];
+                        *reinterpret_cast<half4 *>(a.out_t + base + (int64_t)(col + (lane & 3)) * kp + (row & ~3)) = transpose_quad(o);
                     } else {
-                        const int64_t to = batch * sink.out_batch;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int c = col + e;
-                            if (row < a.sh.k && c < a.sh.len)
-                                sink_one<S, WEIGHT>(sink, to + (a.sh.tall ? (int64_t)c * sink.out_row + row : (int64_t)row * sink.out_row + c), v[e]);
-                        }
+                        sink_four<S, WEIGHT>(sink, a.sh, batch, row, col, v);
                     }
                 }
             }
@@ -344,40 +546,202 @@ __global__ __launch_bounds__(WP *WQ * 64) void ns_product_kernel(NsProduct a, Ns
     }
 }
 
+// ---- 4. small matrices: the whole operator in one workgroup -------------------
+
+// Up to 128 x 128 everything lives in one workgroup: 16 waves of one 32x32 block
+// each, the state in their registers, the half copies of X, its transpose, A
+// and B in LDS (128 KiB). A launch for each product costs more than the
+// products: 17 launches took 120 us for one 128 x 128 matrix, this takes the
+// time of one launch and some 20 us of dependent LDS reads and barriers. A
+// batch is one workgroup a matrix.
+constexpr int kSmall = 128;
+
+// half (row, col) of a 128 x 128 LDS matrix, 16-byte pieces swizzled as above
+__device__ __forceinline__ int small_at(int row, int col) {
+    return row * 256 + (((col >> 3) ^ (row & 15)) << 4) + (col & 7) * 2;
+}
+
+template <class G, bool MOM, class S, bool WEIGHT>
+__global__ __launch_bounds__(1024) void ns_small_kernel(NsSource src, NsSink sink, NsShape sh, int steps, float a, float b,
+                                                        float c, float eps, float x_scale) {
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4][kSmall * kSmall * 2];
+    __shared__ float diag_a[kSmall], diag_b[kSmall];
+    __shared__ double sums[16];
+    uint8_t *xh = lds[0], *xt = lds[1], *am = lds[2], *bm = lds[3];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int batch = blockIdx.x;
+    const int wi = wave >> 2, wj = wave & 3;
+    const int r32 = lane & 31, h = lane >> 5;
+    const int row = wi * 32 + r32;
+    const int col0 = wj * 32 + h * 4;            // value 4 g + e of a lane: column col0 + 8 g + e
+    const bool of_x = wi * 32 < sh.k && wj * 32 < sh.len, of_gram = wi * 32 < sh.k && wj <= wi;
+
+    for (int i = threadIdx.x; i < (int)sizeof(lds) / 16; i += 1024) reinterpret_cast<uint4 *>(&lds[0][0])[i] = uint4{};
+    // the update, and its norm in 64 bits
+    float x[16];
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int col = col0 + (i >> 2) * 8 + (i & 3);
+        const int r = sh.tall ? col : row, q = sh.tall ? row : col;
+        float u = 0.0f;
+        if (row < sh.k && col < sh.len) {
+            u = load_g<G>(src, batch, r, q);
+            if constexpr (MOM) {
+                const int64_t at = batch * src.m_batch + r * src.m_row + q;
+                const float m = __builtin_fmaf(src.beta, src.m[at], u);
+                src.m_out[at] = m;
+                if (src.nesterov)
+                    u = __builtin_fmaf(src.beta, m, u);
+                else
+                    u = m;
+            }
+        }
+        x[i] = u;
+        sum += (double)u * (double)u;
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+    if (lane == 0) sums[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += sums[i];
+    const double inverse = 1.0 / (sqrt(sum) + (double)eps);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = (float)((double)x[i] * inverse);
+
+    auto write_x = [&]() {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            half4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = (_Float16)(x[g * 4 + e] * x_scale);
+            const int col = col0 + g * 8;
+            *reinterpret_cast<half4 *>(xh + small_at(row, col)) = o;
+            *reinterpret_cast<half4 *>(xt + small_at(col + (lane & 3), row & ~3)) = transpose_quad(o);
+        }
+    };
+    // block (wi, wj) of P Q^T over 64 or 128 of depth (what lies beyond is zero), all
+    // operands read before the first is used
+    auto product_of = [&](const uint8_t *p, const uint8_t *q, auto count) {
+        constexpr int N = decltype(count)::value;
+        half8 pf[N], qf[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            pf[k] = *reinterpret_cast<const half8 *>(p + small_at(row, k * 16 + h * 8));
+            qf[k] = *reinterpret_cast<const half8 *>(q + small_at(wj * 32 + r32, k * 16 + h * 8));
+        }
+        float16v acc = {};
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[k], pf[k], acc, 0, 0, 0);
+        return acc;
+    };
+    auto product = [&](const uint8_t *p, const uint8_t *q, int depth) {
+        return depth <= 64 ? product_of(p, q, std::integral_constant<int, 4>()) : product_of(p, q, std::integral_constant<int, 8>());
+    };
+    write_x();
+    __syncthreads();
+    half4 gram[4];
+    for (int s = 0; s < steps; ++s) {
+        if (of_gram) {
+            const float16v acc = product(xh, xh, sh.len);
+            const float factor = kGramScale / (x_scale * x_scale);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int col = col0 + g * 8;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = acc[g * 4 + e] * factor;
+                    if (row == col + e) diag_a[row] = v;
+                    gram[g][e] = row == col + e ? (_Float16)0.0f : (_Float16)v;
+                }
+                *reinterpret_cast<half4 *>(am + small_at(row, col)) = gram[g];
+                if (wi != wj) *reinterpret_cast<half4 *>(am + small_at(col + (lane & 3), row & ~3)) = transpose_quad(gram[g]);
+            }
+        }
+        __syncthreads();
+        if (of_gram) {
+            const float16v acc = product(am, am, sh.k);
+            const float of_row = diag_a[row];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int col = col0 + g * 8;
+                half4 o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = acc[g * 4 + e] * (c / kGramScale);
+                    if (row == col + e)
+                        diag_b[row] = (v + of_row * __builtin_fmaf(of_row, c / kGramScale, b)) / kGramScale;
+                    v = __builtin_fmaf(__builtin_fmaf(of_row + diag_a[col + e], c / kGramScale, b), (float)gram[g][e], v);
+                    o[e] = row == col + e ? (_Float16)0.0f : (_Float16)v;
+                }
+                *reinterpret_cast<half4 *>(bm + small_at(row, col)) = o;
+                if (wi != wj) *reinterpret_cast<half4 *>(bm + small_at(col + (lane & 3), row & ~3)) = transpose_quad(o);
+            }
+        }
+        __syncthreads();
+        if (of_x) {
+            const float16v acc = product(bm, xt, sh.k);
+            const float keep = a + diag_b[row], factor = 1.0f / (kGramScale * x_scale);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf(keep, x[i], acc[i] * factor);
+        }
+        if (s + 1 < steps) {
+            __syncthreads();                     // every wave has read the transpose
+            if (of_x) write_x();
+            __syncthreads();
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float v[4] = {x[g * 4], x[g * 4 + 1], x[g * 4 + 2], x[g * 4 + 3]};
+        sink_four<S, WEIGHT>(sink, sh, batch, row, col0 + g * 8, v);
+    }
+}
+
 int round_to(int64_t v, int t) { return (int)((v + t - 1) / t * t); }
 
-template <int TP, int TQ, int WP, int WQ, int EPI, class S = BF16, bool WEIGHT = false>
+template <int F, int EPI, class S = BF16, bool WEIGHT = false>
 hipError_t launch_product(const NsProduct &a, const NsSink &sink, hipStream_t stream) {
-    const int64_t tiles = EPI == kGram || EPI == kPoly ? (int64_t)a.tiles_p * (a.tiles_p + 1) / 2 : (int64_t)a.tiles_p * a.tiles_q;
-    ns_product_kernel<TP, TQ, WP, WQ, EPI, S, WEIGHT><<<dim3((unsigned)tiles, a.sh.batch), WP * WQ * 64, 0, stream>>>(a, sink);
+    const int tiles = EPI == kGram || EPI == kPoly ? a.tiles_p * (a.tiles_p + 1) / 2 : a.tiles_p * a.tiles_q;
+    ns_product_kernel<F, F, EPI, S, WEIGHT><<<dim3((unsigned)tiles, a.sh.batch), 256, 0, stream>>>(a, sink);
     return hipGetLastError();
 }
 
-template <int EPI>
+template <int EPI, class S = BF16, bool WEIGHT = false>
 hipError_t launch_tiled(const NsProduct &a, const NsSink &sink, hipStream_t stream) {
-    return a.sh.tile == 256 ? launch_product<256, 256, 2, 4, EPI>(a, sink, stream)
-                            : launch_product<128, 128, 2, 2, EPI>(a, sink, stream);
-}
-
-template <class S, bool WEIGHT>
-hipError_t launch_last(const NsProduct &a, const NsSink &sink, hipStream_t stream) {
-    return a.sh.tile == 256 ? launch_product<256, 256, 2, 4, kLast, S, WEIGHT>(a, sink, stream)
-                            : launch_product<128, 128, 2, 2, kLast, S, WEIGHT>(a, sink, stream);
+    return a.sh.tile == 256 ? launch_product<4, EPI, S, WEIGHT>(a, sink, stream)
+                            : launch_product<2, EPI, S, WEIGHT>(a, sink, stream);
 }
 
 template <class G, bool MOM>
 hipError_t launch_prepare(const NsSource &src, const NsShape &sh, const NsLayout &l, uint8_t *ws, float eps,
                           float x_scale, hipStream_t stream) {
     const int64_t total = (int64_t)sh.rows * sh.cols;
+    // 16 elements a lane, until the chip is full
     int parts = (int)((total + 4095) / 4096);
     if (parts > kNsMaxPartials) parts = kNsMaxPartials;
+    const int gs = std::is_same<G, BF16>::value ? 2 : 4;
+    const bool vector = sh.cols % 4 == 0 && reinterpret_cast<uintptr_t>(src.g) % (4 * gs) == 0 && src.g_row % 4 == 0 &&
+                        src.g_batch % 4 == 0 &&
+                        (!MOM || (((reinterpret_cast<uintptr_t>(src.m) | reinterpret_cast<uintptr_t>(src.m_out)) % 16 == 0) &&
+                                  src.m_row % 4 == 0 && src.m_batch % 4 == 0));
     double *partials = reinterpret_cast<double *>(ws + l.partials);
-    ns_norm_kernel<G, MOM><<<dim3(parts, sh.batch), 256, 0, stream>>>(src, sh.rows, sh.cols, partials);
+    ns_norm_kernel<G, MOM><<<dim3(parts, sh.batch), 256, 0, stream>>>(src, sh.rows, sh.cols, vector, partials);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     ns_layout_kernel<G, MOM><<<dim3(sh.kp / 64, sh.lp / 64, sh.batch), 256, 0, stream>>>(
         src, sh, parts, eps, x_scale, partials, reinterpret_cast<float *>(ws + l.x),
         reinterpret_cast<_Float16 *>(ws + l.xh), reinterpret_cast<_Float16 *>(ws + l.xt0));
+    return hipGetLastError();
+}
+
+template <class G, bool MOM, class S, bool WEIGHT>
+hipError_t launch_small(const NsSource &src, const NsSink &sink, const NsShape &sh, int steps, const float *coef, float eps,
+                        float x_scale, hipStream_t stream) {
+    ns_small_kernel<G, MOM, S, WEIGHT><<<sh.batch, 1024, 0, stream>>>(src, sink, sh, steps, coef[0], coef[1], coef[2], eps, x_scale);
     return hipGetLastError();
 }
 
@@ -388,6 +752,16 @@ hipError_t run(const NsSource &src, bool g_bf16, const NsSink &sink, bool out_bf
     float x_scale = 1.0f;
     while (4.0f * x_scale * x_scale <= (float)sh.len) x_scale *= 2.0f;
     const bool mom = src.m != nullptr;
+    if (sh.len <= kSmall) {
+        if (!mom)
+            return g_bf16 ? launch_small<BF16, false, BF16, false>(src, sink, sh, steps, coef, eps, x_scale, stream)
+                          : launch_small<F32, false, BF16, false>(src, sink, sh, steps, coef, eps, x_scale, stream);
+        if (out_bf16)
+            return g_bf16 ? launch_small<BF16, true, BF16, true>(src, sink, sh, steps, coef, eps, x_scale, stream)
+                          : launch_small<F32, true, BF16, true>(src, sink, sh, steps, coef, eps, x_scale, stream);
+        return g_bf16 ? launch_small<BF16, true, F32, true>(src, sink, sh, steps, coef, eps, x_scale, stream)
+                      : launch_small<F32, true, F32, true>(src, sink, sh, steps, coef, eps, x_scale, stream);
+    }
     hipError_t e = g_bf16 ? (mom ? launch_prepare<BF16, true>(src, sh, l, ws, eps, x_scale, stream)
                                  : launch_prepare<BF16, false>(src, sh, l, ws, eps, x_scale, stream))
                           : (mom ? launch_prepare<F32, true>(src, sh, l, ws, eps, x_scale, stream)
@@ -400,7 +774,7 @@ hipError_t run(const NsSource &src, bool g_bf16, const NsSink &sink, bool out_bf
     for (int s = 0; s < steps; ++s) {
         NsProduct a = {};
         a.sh = sh;
-        a.tiles_p = sh.kp / sh.tile;
+        a.tiles_p = (sh.kp + sh.tile - 1) / sh.tile;
         a.tiles_q = a.tiles_p;
         a.p = a.q = xh;
         a.p_batch = a.q_batch = kl;
@@ -423,7 +797,7 @@ hipError_t run(const NsSource &src, bool g_bf16, const NsSink &sink, bool out_bf
         a.q = xt[s & 1];
         a.p_batch = kk;
         a.q_batch = kl;
-        a.tiles_q = sh.lp / sh.tile;
+        a.tiles_q = (sh.lp + sh.tile - 1) / sh.tile;
         a.factor = 1.0f / (kGramScale * x_scale);
         a.a_coef = coef[0];
         a.x_scale = x_scale;
@@ -433,12 +807,17 @@ hipError_t run(const NsSource &src, bool g_bf16, const NsSink &sink, bool out_bf
         if (s + 1 < steps)
             e = launch_tiled<kState>(a, sink, stream);
         else if (!sink.weight)
-            e = launch_last<BF16, false>(a, sink, stream);
+            e = launch_tiled<kLast, BF16, false>(a, sink, stream);
         else
-            e = out_bf16 ? launch_last<BF16, true>(a, sink, stream) : launch_last<F32, true>(a, sink, stream);
+            e = out_bf16 ? launch_tiled<kLast, BF16, true>(a, sink, stream) : launch_tiled<kLast, F32, true>(a, sink, stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+bool groups_aligned(const void *p, const void *q, int64_t batch_stride, int64_t row_stride, int elem) {
+    return (reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) % (4 * elem) == 0 && batch_stride % 4 == 0 &&
+           row_stride % 4 == 0;
 }
 
 bool sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
@@ -475,8 +854,8 @@ NsShape ns_shape(int64_t batch, int64_t rows, int64_t cols) {
     s.k = (int)(rows < cols ? rows : cols);
     s.len = (int)(rows < cols ? cols : rows);
     s.tile = s.k >= 2048 ? 256 : 128;
-    s.kp = round_to(s.k, s.tile);
-    s.lp = round_to(s.len, s.tile);
+    s.kp = round_to(s.k, 64);
+    s.lp = round_to(s.len, 64);
     return s;
 }
 
@@ -528,6 +907,7 @@ int orthogonalize_update(const void *update, void *out, int64_t batch, int64_t r
     sink.out = out;
     sink.out_batch = out_batch_stride;
     sink.out_row = out_row_stride;
+    sink.vector = groups_aligned(out, nullptr, out_batch_stride, out_row_stride, 2);
     const float coef[3] = {a, b, c};
     (void)hipGetLastError();
     return run(src, update_dtype == EWG_BF16, sink, true, ns_shape(batch, rows, cols), steps, coef, eps,
@@ -555,7 +935,8 @@ int muon_step(const void *weight, void *out_weight, const void *main_grad, const
         return EWG_INVALID_ARGUMENT;
     NsSource src = {main_grad, main_grad_batch_stride, main_grad_row_stride, momentum, out_momentum,
                     momentum_batch_stride, momentum_row_stride, beta, nesterov};
-    NsSink sink = {out_weight, weight_batch_stride, weight_row_stride, weight, 1.0f - lr * weight_decay, lr * scale};
+    NsSink sink = {out_weight, weight_batch_stride, weight_row_stride, weight, 1.0f - lr * weight_decay, lr * scale,
+                   groups_aligned(weight, out_weight, weight_batch_stride, weight_row_stride, weight_dtype == EWG_BF16 ? 2 : 4)};
     const float coef[3] = {a, b, c};
     (void)hipGetLastError();
     return run(src, main_grad_dtype == EWG_BF16, sink, weight_dtype == EWG_BF16, ns_shape(batch, rows, cols), steps,
