@@ -302,11 +302,10 @@ __device__ __forceinline__ void sink_four(const NsSink &k, const NsShape &sh, in
     }
 }
 
-// LDS tile: rows of 32 halves, 64 bytes, in four 16-byte pieces; piece c of row
-// r lies at place c ^ (r / 4 % 4), so that sixteen lanes reading one piece of
-// sixteen rows touch each of the 64 banks once (r / 2 % 4, which spreads eight
-// rows over 32 banks, cost four more clocks a read by the conflict counter).
-__device__ __forceinline__ int swizzled(int row, int piece) { return row * 64 + ((piece ^ ((row >> 2) & 3)) << 4); }
+// LDS tile: rows of 64 halves, 128 bytes, in eight 16-byte pieces; piece c of row
+// r lies at place c ^ (r / 2 % 8), so that sixteen lanes reading one piece of
+// sixteen rows touch each of the 64 banks once.
+__device__ __forceinline__ int swizzled(int row, int piece) { return row * 128 + ((piece ^ ((row >> 1) & 7)) << 4); }
 
 typedef int int4v __attribute__((ext_vector_type(4)));
 
@@ -329,29 +328,31 @@ __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
 }
 
-constexpr int kDepth = 32;       // of a stage
+constexpr int kDepth = 64;       // of a stage: rows of 128 bytes, whole lines of the L2
+constexpr int kSteps = kDepth / 16;
 
-// Stages of the LDS ring: 128 KiB for a 256 x 256 tile, 64 for a 128 x 128 one,
-// so that two workgroups of those share a compute unit (a ring of eight and one
-// workgroup: no faster alone, and slower where there are many tiles).
-constexpr int kStages = 4;
+// Stages of the LDS ring, 128 KiB in all. A stage is 2048 clocks of matrix work
+// for a 256 x 256 tile but 512 for a 128 x 128 one, and loads take about 1900
+// to arrive: with a ring of two the small tile took 43 us where it takes 28
+// with four (k 1024, depth 4096), although two workgroups then share a unit.
+template <int FP>
+constexpr int kStages = FP == 4 ? 2 : 4;
 
 // One tile of C = P Q^T, 64 FP x 64 FQ, by four waves of 32 FP x 32 FQ each, kept
-// in registers as 32x32 blocks. P and Q go through a ring of LDS stages of
-// 32 halves of depth, loaded a ring less one ahead; a wave reads the operands of
-// the next 16 of depth from LDS while the matrix instructions of the present 16
-// run, so that one wave a SIMD keeps the matrix unit fed. 128 x 128 a wave
-// rather than 128 x 64 because the LDS is the next bound: a stage's reads and
-// writes take 1536 of its 2048 clocks' worth of matrix work per 64 of depth
-// instead of all 2048. The matrix instruction takes Q as its first operand: a
-// lane then holds four consecutive columns of one row of C.
+// in registers as 32x32 blocks. P and Q go through a ring of LDS stages of 64
+// halves of depth; a wave reads the operands of the next 16 of depth from LDS
+// while the matrix instructions of the present 16 run, so that one wave a SIMD
+// keeps the matrix unit fed. Rows of 64 halves rather than 32: with half lines
+// from the L2 the small tile's products took half as long again. The matrix
+// instruction takes Q as its first operand: a lane then holds four consecutive
+// columns of one row of C.
 template <int FP, int FQ, int EPI, class S, bool WEIGHT>
 __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sink) {
     constexpr int TP = 64 * FP, TQ = 64 * FQ;
-    constexpr int LOADS = (TP + TQ) / 64;            // 1 KiB (16 rows) loads of a wave and stage
-    constexpr int BYTES = (TP + TQ) * 64;
+    constexpr int LOADS = (TP + TQ) / 32;            // 1 KiB (8 rows) loads of a wave and stage
+    constexpr int BYTES = (TP + TQ) * 128;
     constexpr bool SYM = EPI == kGram || EPI == kPoly;
-    constexpr int RING = kStages;
+    constexpr int RING = kStages<FP>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[RING * BYTES];
 
     const int lane = threadIdx.x & 63;
@@ -387,10 +388,10 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
     const int rows_p = a.sh.kp - ti * TP, rows_q = (SYM ? a.sh.kp : a.sh.lp) - tj * TQ;
     const int4v dp = descriptor(a.p + batch * a.p_batch + (int64_t)ti * TP * a.depth, rows_p < TP ? rows_p : TP);
     const int4v dq = descriptor(a.q + batch * a.q_batch + (int64_t)tj * TQ * a.depth, rows_q < TQ ? rows_q : TQ);
-    // Lane l of a load brings piece (l % 4) ^ (l / 16) of row l / 4 of sixteen.
-    // Load i of wave w holds rows 16 (4 i + w): all of a load lie in P or in Q.
-    const int row16 = lane >> 2, piece = (lane & 3) ^ (lane >> 4);
-    const int voffset = (wave * 16 + row16) * a.depth * 2 + piece * 16;
+    // Lane l of a load brings a piece of row l / 8 of eight. Load i of wave w holds
+    // rows 8 (4 i + w): all of a load lie in P or in Q.
+    const int row8 = lane >> 3, piece = (lane & 7) ^ (((wave & 1) << 2) | (row8 >> 1));
+    const int voffset = (wave * 8 + row8) * a.depth * 2 + piece * 16;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + wave * 1024;
     // loads [first, last) of a stage
     auto stage = [&](int t, int first, int last) {
@@ -399,56 +400,62 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
         const uint32_t to = lds0 + (uint32_t)(t & (RING - 1)) * BYTES;
 #pragma unroll
         for (int i = first; i < last; ++i) {
-            const bool in_p = i < FP;
-            load_to_lds(in_p ? dp : dq, voffset, from + (in_p ? i : i - FP) * 64 * a.depth * 2, to + i * 4096);
+            const bool in_p = i < 2 * FP;
+            load_to_lds(in_p ? dp : dq, voffset, from + (in_p ? i : i - 2 * FP) * 32 * a.depth * 2, to + i * 4096);
         }
     };
 
     const int wp = wave & 1, wq = wave >> 1;
     const int r32 = lane & 31, h = lane >> 5;
-    // LDS places of the wave's operands, for the two halves of a stage's depth
-    int p_at[2], q_at[2];
+    // LDS places of the wave's operands, for the steps of a stage's depth
+    int p_at[kSteps], q_at[kSteps];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kSteps; ++s) {
         p_at[s] = swizzled(wp * FP * 32 + r32, s * 2 + h);
-        q_at[s] = TP * 64 + swizzled(wq * FQ * 32 + r32, s * 2 + h);
+        q_at[s] = TP * 128 + swizzled(wq * FQ * 32 + r32, s * 2 + h);
     }
     half8 pf[2][FP], qf[2][FQ];
     float16v acc[FP][FQ] = {};
-    // Half a stage: the matrix instructions of depth half s, block row by block row;
-    // between the rows the reads of the half that comes next and a share of the
-    // loads of a stage to come go out. All eight loads of a wave at once would hold
-    // it up behind the address unit (16 clocks a load) with the matrix unit idle.
+    // Between the block rows of a step's matrix instructions the reads of the step
+    // that comes next and a share of the loads of a stage to come go out. All of a
+    // stage's loads at once hold a wave up behind the address unit with the matrix
+    // unit idle: 428 us instead of 374 for the Gram matrix of 7168 x 7168.
     auto read = [&](const uint8_t *tile, int s, int i) {
-        pf[s][i] = *reinterpret_cast<const half8 *>(tile + p_at[s] + i * 2048);
-        qf[s][i] = *reinterpret_cast<const half8 *>(tile + q_at[s] + i * 2048);
+        pf[s & 1][i] = *reinterpret_cast<const half8 *>(tile + p_at[s] + i * 4096);
+        qf[s & 1][i] = *reinterpret_cast<const half8 *>(tile + q_at[s] + i * 4096);
     };
-    auto half_stage = [&](int s, int next, int load, int first) {
+    // Step s: its products, the reads of the step after (stage `next`), loads [first, last) of stage `load`
+    auto step = [&](int s, int next, int load, int first, int last) {
         const uint8_t *tile = lds + (next & (RING - 1)) * BYTES;
 #pragma unroll
         for (int i = 0; i < FP; ++i) {
-            read(tile, 1 - s, i);
-            stage(load, first + i * LOADS / 2 / FP, first + (i + 1) * LOADS / 2 / FP);
+            read(tile, (s + 1) % kSteps, i);
+            stage(load, first + i * (last - first) / FP, first + (i + 1) * (last - first) / FP);
 #pragma unroll
             for (int j = 0; j < FQ; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[s][j], pf[s][i], acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(qf[s & 1][j], pf[s & 1][i], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    static_assert(FP == FQ && LOADS % 2 == 0, "rows of blocks share out reads and loads evenly");
+    // a stage's loads go out over three steps; the fourth leaves the last of them time
+    constexpr int FIRST = LOADS * 3 / 8, SECOND = LOADS * 6 / 8;
 #pragma unroll
-    for (int t = 0; t < RING - 2; ++t) stage(t, 0, LOADS);
-    stage(RING - 2, 0, LOADS / 2);
-    wait_loads<(RING - 3) * LOADS + LOADS / 2>();
+    for (int t = 0; t < RING - 1; ++t) stage(t, 0, LOADS);
+    stage(RING - 1, 0, FIRST);
+    wait_loads<(RING - 2) * LOADS + FIRST>();
     __builtin_amdgcn_s_barrier();
 #pragma unroll
     for (int i = 0; i < FP; ++i) read(lds, 0, i);
     for (int t = 0; t < stages; ++t) {
-        half_stage(0, t, t + RING - 2, LOADS / 2);
-        // stage t + 1 is there for every wave, and every wave has read stage t - 1
-        wait_loads<(RING - 3) * LOADS>();
+        // the loads of stage t + RING - 1 go on from the last step of the stage before
+        step(0, t, t + RING - 1, FIRST, SECOND);
+        step(1, t, t + RING - 1, SECOND, LOADS);
+        step(2, t, t + RING - 1, LOADS, LOADS);
+        // stage t + 1 is there for every wave, and every wave has read all of stage t
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_loads<(RING - 2) * LOADS>();
         __builtin_amdgcn_s_barrier();
-        half_stage(1, t + 1, t + RING - 1, 0);
+        step(3, t + 1, t + RING, 0, FIRST);
     }
     wait_loads<0>();
 
