@@ -42,7 +42,7 @@ extern "C" {
 /* Bounds; EWG_UNSUPPORTED outside them. */
 #define EWG_MAX_TOP_LOGPROBS 32
 #define EWG_LOGPROBS_MAX_ROWS 1048576
-#define EWG_LOGPROBS_MAX_VOCAB 4194304
+#define EWG_LOGPROBS_MAX_VOCAB 1048576
 
 /* Bytes of workspace token_logprobs needs (host only; 0 if out of range, or if
  * it needs none: rows are split over workgroups, and the parts kept in the

@@ -9,7 +9,7 @@ from ._binding import DTYPE_CODE, EWG_OK, EmbeddingWgradError, _stream_handle, l
 
 MAX_TOP_LOGPROBS = 32             # EWG_MAX_TOP_LOGPROBS
 MAX_ROWS = 1048576                # EWG_LOGPROBS_MAX_ROWS
-MAX_VOCAB = 4194304               # EWG_LOGPROBS_MAX_VOCAB
+MAX_VOCAB = 1048576               # EWG_LOGPROBS_MAX_VOCAB
 
 _i64, _int, _vp, _sz, _f32 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
 

@@ -10,12 +10,18 @@
 // w holds distances to the maximum, not the logits themselves, so nothing
 // cancels in the entropy of a peaked row.
 //
-// The pass reads rows in groups of 64 16-byte pieces (one wave load). For the
-// alternatives it keeps nothing per element: only each group's maximum, in
-// LDS. The top_k largest elements lie in the top_k groups with the largest
-// maxima (equal ones by the lower index: groups are contiguous, so that is
-// the order of their first largest elements too), and by the same argument in
-// the top_k largest pieces of those groups; these few are read again.
+// For the alternatives the pass keeps nothing per element: only the maximum of
+// each group of sixteen 16-byte pieces (256 bytes), which costs four DPP steps
+// a wave load. Of these maxima, dealt to the 256 lanes of a workgroup, the
+// top_k-th largest lane's is a lower bound on the top_k-th largest element, and
+// a close one (a few lanes hold two of the largest); only the groups that reach
+// it are read again, and the two or three dozen elements above it are ranked
+// against each other. Elements equal to it are taken in index order.
+//
+// A row is one workgroup's where there are many, so that nothing but the
+// results is written. Few rows are cut into parts of one set of loads a wave;
+// the parts leave their states and group maxima in the workspace, and a second
+// kernel, one workgroup a row, joins them and finds the alternatives once.
 //
 // Backward, one pass that reads the logits and writes the gradient.
 #include <hip/hip_runtime.h>
@@ -33,9 +39,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kUnroll = 4;             // groups a wave has in flight
-constexpr int kMaxGroups = 1024;       // group maxima one workgroup keeps
-constexpr int kMaxSplits = 64;         // parts of a row: one lane each in the join
+constexpr int kGroupLanes = 16;        // pieces of a group
+constexpr int kRowGroups = 2048;       // group maxima a workgroup keeps for a whole row
+constexpr int kMaxGroups = 16640;      // of the largest row (4-byte logits), 64 KiB of LDS
+constexpr int kFewGroups = 4096;       // rows of fewer take less LDS in the join
 constexpr int kMaxTopK = EWG_MAX_TOP_LOGPROBS;
+static_assert(kMaxGroups >= (EWG_LOGPROBS_MAX_VOCAB + 3 + 255) / 256 * 4, "the largest row's groups fit");
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kMasked = -1e38f;      // logits at or below are masked, the types' lowest values among them
@@ -94,12 +103,16 @@ __device__ __forceinline__ int dpp(int v) {
     return __builtin_amdgcn_update_dpp(v, v, CTRL, ROWS, 0xf, false);
 }
 
-// maximum / minimum over the wave, the same in every lane
-__device__ __forceinline__ float wave_max(float v) {
+// maximum over the sixteen lanes of a DPP row, in each of them
+__device__ __forceinline__ float row_max(float v) {
     v = max2(v, dpp<0x128>(v));
     v = max2(v, dpp<0x124>(v));
     v = max2(v, dpp<0x122>(v));
-    v = max2(v, dpp<0x121>(v));
+    return max2(v, dpp<0x121>(v));
+}
+// maximum, minimum, sum over the wave, the same in every lane
+__device__ __forceinline__ float wave_max(float v) {
+    v = row_max(v);
     v = max2(v, dpp<0x142, 0xa>(v));
     v = max2(v, dpp<0x143, 0xc>(v));
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
@@ -113,23 +126,31 @@ __device__ __forceinline__ int wave_min(int v) {
     v = min(v, dpp<0x143, 0xc>(v));
     return __builtin_amdgcn_readlane(v, 63);
 }
-
-// Joins two states. A state of nothing has m = -inf and s = w = 0.
-__device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
-    const float m = max2(a.m, b.m);
-    const float da = a.m == kNegInf ? 0.0f : (a.m - m) * c, db = b.m == kNegInf ? 0.0f : (b.m - m) * c;
-    const float ea = exp2f(da), eb = exp2f(db);
-    return {m, __builtin_fmaf(a.s, ea, b.s * eb),
-            __builtin_fmaf(ea, __builtin_fmaf(a.s, da, a.w), eb * __builtin_fmaf(b.s, db, b.w))};
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_zero(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp<0x128>(v);
+    v += dpp<0x124>(v);
+    v += dpp<0x122>(v);
+    v += dpp<0x121>(v);
+    v += dpp_or_zero<0x142, 0xa>(v);
+    v += dpp_or_zero<0x143, 0xc>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// A state against a larger maximum. A state of nothing has m = -inf, s = w = 0.
+__device__ __forceinline__ Stat rebased(Stat a, float m, float c) {
+    const float d = a.m == kNegInf ? 0.0f : (a.m - m) * c;
+    const float e = __builtin_amdgcn_exp2f(d);
+    return {m, a.s * e, e * __builtin_fmaf(a.s, d, a.w)};
+}
+
+// The states of a wave's lanes joined, in every lane.
 __device__ __forceinline__ Stat join_wave(Stat a, float c) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const Stat b = {__shfl_xor(a.m, o), __shfl_xor(a.s, o), __shfl_xor(a.w, o)};
-        a = join(a, b, c);
-    }
-    return a;
+    a = rebased(a, wave_max(a.m), c);
+    return {a.m, wave_sum(a.s), wave_sum(a.w)};
 }
 
 struct RowOut {
@@ -137,11 +158,10 @@ struct RowOut {
     int64_t *top_ids;
 };
 
-// The numbers of a row from its joined state. Returns logsumexp; ln_s is 0
-// for a row with nothing left.
-template <class T>
-__device__ __forceinline__ float finish_row(const RowOut &o, int64_t row, Stat t, const typename T::T *x,
-                                            int64_t target, int64_t vocab, float inv_t, float &ln_s) {
+// The numbers of a row from its joined state and its target's logit. Returns
+// logsumexp; ln_s is 0 for a row with nothing left.
+__device__ __forceinline__ float finish_row(const RowOut &o, int64_t row, Stat t, float xt, int64_t target, int64_t vocab,
+                                            float inv_t, bool write, float &ln_s) {
     ln_s = t.m == kNegInf && t.s == 0.0f ? 0.0f : kLn2 * log2f(t.s);
     float lse = t.m * inv_t + ln_s;
     float entropy = t.s == 0.0f ? 0.0f : __builtin_fmaf(-kLn2, t.w / t.s, ln_s);
@@ -153,140 +173,216 @@ __device__ __forceinline__ float finish_row(const RowOut &o, int64_t row, Stat t
     } else if (target >= vocab) {
         lp = __builtin_nanf("");
     } else {
-        const float xt = T::widen(x[target]);
         lp = xt <= kMasked ? kNegInf : __builtin_fmaf(xt - t.m, inv_t, -ln_s);
     }
     if (bad) {
         lse = entropy = __builtin_nanf("");
         if (target >= 0) lp = lse;
     }
-    o.logprobs[row] = lp;
-    o.entropy[row] = entropy;
-    o.logsumexp[row] = lse;
+    if (write) {
+        o.logprobs[row] = lp;
+        o.entropy[row] = entropy;
+        o.logsumexp[row] = lse;
+    }
     return lse;
 }
 
-// Marks the k largest of n values (n <= 64 * kept) in LDS, equal ones by the
-// lower index first, by setting bit 0 of flags; values are consumed. One wave.
-__device__ __forceinline__ void select_top(float *values, uint8_t *flags, int n, int k) {
-    const int lane = threadIdx.x & 63;
-    float best = kNegInf;
-    int at = n;
-    auto scan = [&]() {
-        best = kNegInf;
-        at = 0x7fffffff;
-        for (int i = lane; i < n; i += 64) {
-            const float v = values[i];
-            if (v > best) {
-                best = v;
-                at = i;
-            }
-        }
-    };
-    for (int i = lane; i < n; i += 64) flags[i] = 0;
-    scan();
-    for (int r = 0; r < k; ++r) {
-        const float top = wave_max(best);
-        if (top == kNegInf) break;
-        const int first = wave_min(best == top ? at : 0x7fffffff);
-        if (at == first) {
-            values[first] = kNegInf;
-            flags[first] = 1;
-            scan();
-        }
-    }
-}
+constexpr int kCandidates = 256;       // elements above the bound that are ranked
 
-// Indexes of the set flags, ascending, into list; returns how many.
-__device__ __forceinline__ int collect(const uint8_t *flags, int n, uint16_t *list) {
-    const int lane = threadIdx.x & 63;
-    int count = 0;
-    for (int base = 0; base < n; base += 64) {
-        const bool on = base + lane < n && flags[base + lane];
-        const uint64_t who = __ballot(on);
-        if (on) list[count + __popcll(who & ((1ull << lane) - 1))] = (uint16_t)(base + lane);
-        count += __popcll(who);
-    }
-    return count;
-}
-
+template <int GROUPS>
 struct TopScratch {
-    float group_max[kMaxGroups];
-    float piece_max[kMaxTopK * 64];
-    uint8_t flags[kMaxTopK * 64];
-    uint16_t list[kMaxTopK * 64];
-    uint16_t groups[kMaxTopK];
+    float group_max[GROUPS];
+    uint16_t list[GROUPS];             // groups that reach the bound
+    float lane_max[kThreads];
+    float value[kCandidates];
+    int index[kCandidates];
+    float best[kMaxTopK];
+    int best_at[kMaxTopK];
+    int listed, count;
 };
-static_assert(kMaxGroups <= kMaxTopK * 64, "flags and list hold either");
 
-// The top_k largest of groups [g0, g0 + n), in order; lane r of wave 0 ends
-// with the r-th (value -inf where there is none). Wave 0 only, after a
-// barrier behind the group maxima.
+// The lane's piece of four listed groups from list[j] on; masked logits as -inf,
+// as are the lanes past the list.
 template <class T>
-__device__ __forceinline__ void top_of_part(TopScratch &t, const typename T::T *row, int lead, int vocab, int g0, int n,
-                                            int k, float &value, int &index) {
+__device__ __forceinline__ int load_listed(const typename T::T *row, int lead, int vocab, const uint16_t *list, int j, int listed,
+                                           float (&v)[kPiece<T>]) {
     constexpr int E = kPiece<T>;
     const int lane = threadIdx.x & 63;
-    // the k-th largest group maximum bounds the k-th largest element from below
-    int picked;
-    if (n > k) {
-        select_top(t.group_max, t.flags, n, k);
-        picked = collect(t.flags, n, t.list);
-    } else {
-        for (int i = lane; i < n; i += 64) t.list[i] = (uint16_t)i;
-        picked = n;
-    }
-    if (lane < picked) t.groups[lane] = t.list[lane];
-    // maxima of the 64 pieces of each picked group, in index order
-    for (int j = 0; j < picked; ++j) {
-        float v[E];
-        load_piece<T>(row, ((int64_t)(g0 + t.groups[j]) * 64 + lane) * E - lead, vocab, v);
-        float m = v[0];
-#pragma unroll
-        for (int e = 1; e < E; ++e) m = max2(m, v[e]);
-        t.piece_max[j * 64 + lane] = m > kMasked ? m : kNegInf;
-    }
-    select_top(t.piece_max, t.flags, picked * 64, k);
-    const int pieces = collect(t.flags, picked * 64, t.list);
-    // at most one piece a lane: its elements
-    float v[E];
-    int64_t first = 0;
-    if (lane < pieces) {
-        const int p = t.list[lane];
-        first = ((int64_t)(g0 + t.groups[p >> 6]) * 64 + (p & 63)) * E - lead;
+    j += lane / kGroupLanes;
+    int first = 0;
+    if (j < listed) {
+        first = (list[j] * kGroupLanes + lane % kGroupLanes) * E - lead;
         load_piece<T>(row, first, vocab, v);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = v[e] > kMasked ? v[e] : kNegInf;
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = kNegInf;
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = j < listed && v[e] > kMasked ? v[e] : kNegInf;
+    return first;
+}
+
+constexpr int kWaveGroups = 64 / kGroupLanes;
+
+// The candidates of the listed groups: elements above the bound, or at it too.
+template <class T, bool EQUAL, int GROUPS>
+__device__ __forceinline__ void collect(TopScratch<GROUPS> &t, const typename T::T *row, int lead, int vocab, float bound) {
+    constexpr int E = kPiece<T>;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int listed = t.listed;
+    for (int j = wave * kWaveGroups; j < listed; j += kWaves * kWaveGroups) {
+        float v[E];
+        const int first = load_listed<T>(row, lead, vocab, t.list, j, listed, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (v[e] > bound || (EQUAL && v[e] == bound && v[e] > kNegInf)) {
+                const int at = atomicAdd(&t.count, 1);
+                if (at < kCandidates) {
+                    t.value[at] = v[e];
+                    t.index[at] = first + e;
+                }
+            }
+    }
+}
+
+// The k largest of a row's n groups, in order; lane r of wave 0 ends with the
+// r-th (value -inf, index -1 where there is none). The whole workgroup, after a
+// barrier behind the group and lane maxima.
+template <class T, int GROUPS>
+__device__ __forceinline__ void top_of_row(TopScratch<GROUPS> &t, const typename T::T *row, int lead, int vocab, int n, int k,
+                                           float &value, int &index) {
+    constexpr int E = kPiece<T>;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     value = kNegInf;
     index = -1;
-    for (int r = 0; r < k; ++r) {
-        float best = v[0];
-        int e_best = 0;
+    // The bound, in every wave: the k-th largest of 64 maxima of a quarter-lane's
+    // each. (Of all 256 it would be little closer: of 20 wanted, 24 elements reach
+    // this one.)
+    float m = t.lane_max[lane];
 #pragma unroll
-        for (int e = 1; e < E; ++e)
-            if (v[e] > best) {
-                best = v[e];
-                e_best = e;
+    for (int i = 1; i < kWaves; ++i) m = max2(m, t.lane_max[i * 64 + lane]);
+    int above = 0, reach = 0;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+        const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(m), j));
+        above += w > m;
+        reach += w >= m;
+    }
+    const uint64_t who = __ballot(above < k && k <= reach);
+    const float bound = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(m), who ? __ffsll((unsigned long long)who) - 1 : 0));
+    auto reaches = [&](int g) {
+        const float v = g < n ? t.group_max[g] : kNegInf;
+        return v >= bound && v > kNegInf;
+    };
+    if (threadIdx.x == 0) t.listed = t.count = 0;
+    if (threadIdx.x < kMaxTopK) {
+        t.best[threadIdx.x] = kNegInf;
+        t.best_at[threadIdx.x] = -1;
+    }
+    __syncthreads();
+    for (int base = wave * 64; base < n; base += kThreads) {
+        const bool on = reaches(base + lane);
+        const uint64_t hits = __ballot(on);
+        if (hits == 0) continue;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&t.listed, __popcll(hits));
+        at = __builtin_amdgcn_readfirstlane(at);
+        if (on) t.list[at + __popcll(hits & ((1ull << lane) - 1))] = (uint16_t)(base + lane);
+    }
+    __syncthreads();
+    collect<T, true>(t, row, lead, vocab, bound);
+    __syncthreads();
+    if (t.count > kCandidates) {
+        // A great many equal the bound, or a few lanes hold a great many of the largest.
+        // The elements above the bound alone, and the groups in order.
+        __syncthreads();
+        if (threadIdx.x == 0) t.count = 0;
+        __syncthreads();
+        collect<T, false>(t, row, lead, vocab, bound);
+        __syncthreads();
+        if (wave != 0) return;
+        int listed = 0;
+        for (int base = 0; base < n; base += 64) {
+            const bool on = reaches(base + lane);
+            const uint64_t hits = __ballot(on);
+            if (on) t.list[listed + __popcll(hits & ((1ull << lane) - 1))] = (uint16_t)(base + lane);
+            listed += __popcll(hits);
+        }
+        int count = t.count;
+        if (count > kCandidates) {
+            // one element a round, the best after the one before
+            float before = __builtin_inff();
+            int before_at = -1;
+            for (int r = 0; r < k; ++r) {
+                float best = kNegInf;
+                int at = 0x7fffffff;
+                for (int j = 0; j < listed; j += kWaveGroups) {
+                    float v[E];
+                    const int first = load_listed<T>(row, lead, vocab, t.list, j, listed, v);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const int i = first + e;
+                        if ((v[e] < before || (v[e] == before && i > before_at)) && v[e] > best) {
+                            best = v[e];
+                            at = i;
+                        }
+                    }
+                }
+                const float top = wave_max(best);
+                if (top == kNegInf) break;
+                before_at = wave_min(best == top ? at : 0x7fffffff);
+                before = top;
+                if (lane == r) {
+                    value = before;
+                    index = before_at;
+                }
             }
-        const float top = wave_max(best);
-        if (top == kNegInf) break;
-        const uint64_t who = __ballot(best == top);
-        const int owner = __ffsll((unsigned long long)who) - 1;     // pieces are in index order
-        const int at = (int)first + e_best;
-        const int won = __builtin_amdgcn_readlane(at, owner);
-        if (lane == owner) {
+            return;
+        }
+        // those equal to the bound, in index order, as many as are wanted
+        for (int j = 0; j < listed && count < k; j += kWaveGroups) {
+            float v[E];
+            const int first = load_listed<T>(row, lead, vocab, t.list, j, listed, v);
+            int mine = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) mine += v[e] == bound && v[e] > kNegInf;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int below = __shfl_up(upto, o);
+                if (lane >= o) upto += below;
+            }
+            int at = count + upto - mine;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (e == e_best) v[e] = kNegInf;
+                if (v[e] == bound && v[e] > kNegInf && at < k) {
+                    t.value[at] = bound;
+                    t.index[at] = first + e;
+                    ++at;
+                }
+            count += __shfl(upto, 63);
+            if (count > k) count = k;
         }
-        if (lane == r) {
-            value = top;
-            index = won;
+        if (lane == 0) t.count = count;
+    }
+    if (wave != 0) return;
+    // rank each against all
+    const int count = __builtin_amdgcn_readfirstlane(t.count);
+    for (int c = lane; c < count; c += 64) {
+        const float v = t.value[c];
+        const int i = t.index[c];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < count; ++j) {
+            const float w = t.value[j];
+            rank += w > v || (w == v && t.index[j] < i);
         }
+        if (rank < k) {
+            t.best[rank] = v;
+            t.best_at[rank] = i;
+        }
+    }
+    if (lane < k) {
+        value = t.best[lane];
+        index = t.best_at[lane];
     }
 }
 
@@ -296,41 +392,61 @@ struct Forward {
     const void *targets;
     int targets64;
     int64_t rows;
-    int vocab, splits, groups_per_split, top_k;
+    int vocab, splits, loads_per_split, top_k;
     float c, inv_t;            // log2(e) / T and 1 / T
     RowOut out;
     Stat *stats;               // [rows][splits] where splits > 1
-    float *part_values;        // [rows][splits][top_k]
-    int *part_ids;
+    float *group_max;          // [rows][groups], likewise
+    int groups;                // of a row, at any lead
 };
 
 __device__ __forceinline__ int64_t target_of(const void *targets, int is64, int64_t row) {
     return is64 ? static_cast<const int64_t *>(targets)[row] : static_cast<const int32_t *>(targets)[row];
 }
 
-template <class T, bool TOP>
+// The results of a row, by wave 0: lanes 0..top_k-1 hold the alternatives.
+template <bool TOP>
+__device__ __forceinline__ void write_row(const Forward &f, int64_t row, Stat t, int64_t target, float xt, float value, int index) {
+    const int lane = threadIdx.x & 63;
+    float ln_s;
+    const float lse = finish_row(f.out, row, t, xt, target, f.vocab, f.inv_t, lane == 0, ln_s);
+    if (TOP && lane < f.top_k) {
+        const bool none = index < 0 || lse != lse;
+        f.out.top_logprobs[row * f.top_k + lane] = lse != lse ? lse : none ? kNegInf : __builtin_fmaf(value - t.m, f.inv_t, -ln_s);
+        f.out.top_ids[row * f.top_k + lane] = none ? -1 : index;
+    }
+}
+
+// One part of a row, or the whole of it (PARTS false). A wave load is 64 pieces;
+// a wave takes sets of kUnroll loads in turn with the others.
+template <class T, bool TOP, bool PARTS>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(Forward f) {
     constexpr int E = kPiece<T>;
     using V = typename T::T;
     __shared__ Stat stats[kWaves];
-    __shared__ typename std::conditional<TOP, TopScratch, int>::type scratch;
+    __shared__ typename std::conditional<TOP && !PARTS, TopScratch<kRowGroups>, int>::type scratch;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = row_of_block();
     if (row >= f.rows) return;
-    const int split = blockIdx.x;
     const V *x = static_cast<const V *>(f.logits) + row * f.row_stride;
     const int lead = lead_of<T>(x);
-    const int groups = (int)(((int64_t)lead + f.vocab + 64 * E - 1) / (64 * E));
-    const int g0 = split * f.groups_per_split;
-    int n = groups - g0;
-    if (n > f.groups_per_split) n = f.groups_per_split;
+    const int loads = (lead + f.vocab + 64 * E - 1) / (64 * E);
+    const int g0 = PARTS ? blockIdx.x * f.loads_per_split : 0;
+    int n = loads - g0;
+    if (PARTS && n > f.loads_per_split) n = f.loads_per_split;
+    // asked for now, needed at the end
+    int64_t target = -1;
+    float xt = 0.0f;
+    if constexpr (!PARTS) {
+        target = target_of(f.targets, f.targets64, row);
+        if (target >= 0 && target < f.vocab) xt = T::widen(x[target]);
+    }
 
     Stat t = {kNegInf, 0.0f, 0.0f};
-    // a set: kUnroll groups a wave, one after another
     for (int g = wave * kUnroll; g < n; g += kWaves * kUnroll) {
         float v[kUnroll][E];
-        const int64_t from = (int64_t)(g0 + g) * 64 * E - lead;
+        const int from = (g0 + g) * 64 * E - lead;
         if (g + kUnroll <= n && from >= 0 && from + kUnroll * 64 * E <= f.vocab) {
             // inside the row, the same for the whole wave: the loads go out back to back
             V raw[kUnroll][E];
@@ -360,12 +476,18 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(Forward f) {
             m = m > kMasked ? m : kNegInf;
             top = max2(top, m);
             if constexpr (TOP) {
-                const float all = wave_max(m);
-                if (lane == 0 && g + u < n) scratch.group_max[g + u] = all;
+                const float all = row_max(m);
+                if (lane % kGroupLanes == 0 && g + u < n) {
+                    const int group = (g0 + g + u) * kWaveGroups + lane / kGroupLanes;
+                    if constexpr (PARTS)
+                        f.group_max[row * f.groups + group] = all;
+                    else
+                        scratch.group_max[group] = all;
+                }
             }
         }
         const float d = t.m == kNegInf ? 0.0f : (t.m - top) * f.c;
-        const float scale = exp2f(d);
+        const float scale = __builtin_amdgcn_exp2f(d);
         t.w = scale * __builtin_fmaf(t.s, d, t.w);
         t.s *= scale;
         t.m = top;
@@ -376,90 +498,68 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(Forward f) {
         for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                // the clamp keeps 0 * -inf out of w; it passes NaN to exp2 and so to s
+                // the clamp keeps 0 * -inf out of w; NaN goes through exp2 into s
                 const float y = (v[u][e] - base) * f.c;
                 const float p = __builtin_amdgcn_exp2f(y);
                 t.s += p;
                 t.w = __builtin_fmaf(p, max2(y, -3.0e38f), t.w);
             }
     }
+    if constexpr (TOP && !PARTS) scratch.lane_max[threadIdx.x] = t.m;
     t = join_wave(t, f.c);
     if (lane == 0) stats[wave] = t;
     __syncthreads();
-    if (wave != 0) return;
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) t = join(t, stats[i], f.c);
-
     float value = kNegInf;
     int index = -1;
-    if constexpr (TOP) top_of_part<T>(scratch, x, lead, f.vocab, g0, n, f.top_k, value, index);
-    if (f.splits > 1) {
-        if (lane == 0) f.stats[row * f.splits + split] = t;
-        if (TOP && lane < f.top_k) {
-            f.part_values[(row * f.splits + split) * f.top_k + lane] = value;
-            f.part_ids[(row * f.splits + split) * f.top_k + lane] = index;
-        }
-        return;
-    }
-    float ln_s = 0.0f, lse = 0.0f;
-    if (lane == 0) lse = finish_row<T>(f.out, row, t, x, target_of(f.targets, f.targets64, row), f.vocab, f.inv_t, ln_s);
-    if constexpr (TOP) {
-        ln_s = __shfl(ln_s, 0);
-        lse = __shfl(lse, 0);
-        if (lane < f.top_k) {
-            const bool none = index < 0 || lse != lse;
-            f.out.top_logprobs[row * f.top_k + lane] =
-                lse != lse ? lse : none ? kNegInf : __builtin_fmaf(value - t.m, f.inv_t, -ln_s);
-            f.out.top_ids[row * f.top_k + lane] = none ? -1 : index;
-        }
+    if constexpr (TOP && !PARTS) top_of_row<T>(scratch, x, lead, f.vocab, loads * kWaveGroups, f.top_k, value, index);
+    if (wave != 0) return;
+    t = join_wave(lane < kWaves ? stats[lane] : Stat{kNegInf, 0.0f, 0.0f}, f.c);
+    if constexpr (PARTS) {
+        if (lane == 0) f.stats[row * f.splits + blockIdx.x] = t;
+    } else {
+        write_row<TOP>(f, row, t, target, xt, value, index);
     }
 }
 
-// Joins the parts of a row: one wave a row, one lane a part.
-template <class T, bool TOP>
-__global__ __launch_bounds__(64) void logprobs_join_kernel(Forward f) {
+// Joins the parts of a row.
+template <class T, bool TOP, int GROUPS>
+__global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Forward f) {
     using V = typename T::T;
-    const int lane = threadIdx.x;
+    __shared__ Stat stats[kWaves];
+    __shared__ typename std::conditional<TOP, TopScratch<GROUPS>, int>::type scratch;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = row_of_block();
     if (row >= f.rows) return;
-    Stat t = {kNegInf, 0.0f, 0.0f};
-    if (lane < f.splits) t = f.stats[row * f.splits + lane];
-    t = join_wave(t, f.c);
     const V *x = static_cast<const V *>(f.logits) + row * f.row_stride;
-    float ln_s = 0.0f, lse = 0.0f;
-    if (lane == 0) lse = finish_row<T>(f.out, row, t, x, target_of(f.targets, f.targets64, row), f.vocab, f.inv_t, ln_s);
+    const int lead = lead_of<T>(x);
+    const int64_t target = target_of(f.targets, f.targets64, row);
+    float xt = 0.0f;
+    if (target >= 0 && target < f.vocab) xt = T::widen(x[target]);
+    // part i is lane i's; there are at most kThreads
+    Stat t = {kNegInf, 0.0f, 0.0f};
+    if ((int)threadIdx.x < f.splits) t = f.stats[row * f.splits + threadIdx.x];
+    t = join_wave(t, f.c);
+    if (lane == 0) stats[wave] = t;
+    float value = kNegInf;
+    int index = -1;
     if constexpr (TOP) {
-        ln_s = __shfl(ln_s, 0);
-        lse = __shfl(lse, 0);
-        // every part's alternatives are in order; parts are in index order
-        const int64_t base = (row * f.splits + lane) * f.top_k;
-        int taken = 0;
-        float head = lane < f.splits ? f.part_values[base] : kNegInf;
-        float value = kNegInf;
-        int index = -1;
-        for (int r = 0; r < f.top_k; ++r) {
-            const float top = wave_max(head);
-            if (top == kNegInf) break;
-            const int owner = __ffsll((unsigned long long)__ballot(head == top)) - 1;
-            int id = 0;
-            if (lane == owner) {
-                id = f.part_ids[base + taken];
-                ++taken;
-                head = taken < f.top_k ? f.part_values[base + taken] : kNegInf;
-            }
-            id = __builtin_amdgcn_readlane(id, owner);
-            if (lane == r) {
-                value = top;
-                index = id;
-            }
+        const int n = (lead + f.vocab + 64 * kPiece<T> - 1) / (64 * kPiece<T>) * kWaveGroups;
+        float m = kNegInf;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const float g = f.group_max[row * f.groups + i];
+            scratch.group_max[i] = g;
+            m = max2(m, g);
         }
-        if (lane < f.top_k) {
-            const bool none = index < 0 || lse != lse;
-            f.out.top_logprobs[row * f.top_k + lane] =
-                lse != lse ? lse : none ? kNegInf : __builtin_fmaf(value - t.m, f.inv_t, -ln_s);
-            f.out.top_ids[row * f.top_k + lane] = none ? -1 : index;
-        }
+        scratch.lane_max[threadIdx.x] = m;
+        __syncthreads();
+        top_of_row<T>(scratch, x, lead, f.vocab, n, f.top_k, value, index);
+    } else {
+        __syncthreads();
     }
+    if (wave != 0) return;
+    t = join_wave(lane < kWaves ? stats[lane] : Stat{kNegInf, 0.0f, 0.0f}, f.c);
+    write_row<TOP>(f, row, t, target, xt, value, index);
 }
 
 // ---- backward -----------------------------------------------------------------
@@ -565,8 +665,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(Backward f)
 // ---- host ---------------------------------------------------------------------
 
 struct Plan {
-    int splits, groups_per_split;
-    size_t stats, values, ids, total;
+    int splits, loads_per_split, groups;
+    size_t stats, group_max, total;
 };
 
 int compute_units() {
@@ -580,24 +680,28 @@ int compute_units() {
     return v;
 }
 
-// Parts of a row: about four workgroups a compute unit in all when there are
-// few rows, but no part below one set of a workgroup's waves (four groups),
-// and no part above the group maxima a workgroup keeps. cus: the device's.
+// One workgroup a row where that fills the chip (two rows a compute unit) and
+// the row's group maxima fit; otherwise parts of one set of loads a wave, or as
+// many sets as keep a row to 256 parts and the chip to about eight parts a unit.
 Plan plan_for(int64_t rows, int64_t vocab, int elem, int top_k, int cus) {
     const int64_t per = 64 * (16 / elem);
-    const int64_t groups = (vocab + 16 / elem - 1 + per - 1) / per;     // the most any lead gives
-    int64_t splits = rows > 0 ? (4 * (int64_t)cus + rows - 1) / rows : 1;
-    if (splits > (groups + kWaves - 1) / kWaves) splits = (groups + kWaves - 1) / kWaves;
-    if (splits > kMaxSplits) splits = kMaxSplits;
-    if (splits < (groups + kMaxGroups - 1) / kMaxGroups) splits = (groups + kMaxGroups - 1) / kMaxGroups;
-    if (splits < 1) splits = 1;
-    Plan p;
-    p.groups_per_split = (int)((groups + splits - 1) / splits);
-    p.splits = (int)((groups + p.groups_per_split - 1) / p.groups_per_split);
+    const int64_t loads = (vocab + 16 / elem - 1 + per - 1) / per;      // the most any lead gives
+    Plan p = {};
+    p.groups = (int)loads * kWaveGroups;
+    p.splits = 1;
+    p.loads_per_split = (int)loads;
+    const bool fits = top_k == 0 || p.groups <= kRowGroups;
+    const int64_t set = kWaves * kUnroll;
+    if ((rows >= 2 * (int64_t)cus && fits) || (loads <= set && fits)) return p;
+    int64_t splits = (loads + set - 1) / set;
+    if (splits * rows > 8 * (int64_t)cus) splits = (8 * (int64_t)cus + rows - 1) / rows;
+    if (splits > kThreads) splits = kThreads;
+    if (splits < 2) splits = 2;
+    p.loads_per_split = (int)(((loads + splits - 1) / splits + kUnroll - 1) / kUnroll * kUnroll);
+    p.splits = (int)((loads + p.loads_per_split - 1) / p.loads_per_split);
     p.stats = 0;
-    p.values = p.splits > 1 ? round_up(sizeof(Stat) * (size_t)rows * p.splits, 256) : 0;
-    p.ids = p.splits > 1 ? round_up(p.values + 4 * (size_t)rows * p.splits * top_k, 256) : 0;
-    p.total = p.splits > 1 ? round_up(p.ids + 4 * (size_t)rows * p.splits * top_k, 256) : 0;
+    p.group_max = round_up(sizeof(Stat) * (size_t)rows * p.splits, 256);
+    p.total = round_up(p.group_max + (top_k ? 4 * (size_t)rows * p.groups : 0), 256);
     return p;
 }
 
@@ -615,11 +719,18 @@ int check_sizes(int64_t rows, int64_t vocab, int64_t stride, int logits_dtype, i
 }
 
 template <class T, bool TOP>
-hipError_t launch_forward(const Forward &f, hipStream_t stream) {
-    logprobs_kernel<T, TOP><<<grid_of(f.splits, f.rows), kThreads, 0, stream>>>(f);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || f.splits == 1) return e;
-    logprobs_join_kernel<T, TOP><<<grid_of(1, f.rows), 64, 0, stream>>>(f);
+hipError_t launch_forward(const Forward &f, bool parts, hipStream_t stream) {
+    if (!parts) {
+        logprobs_kernel<T, TOP, false><<<grid_of(1, f.rows), kThreads, 0, stream>>>(f);
+        return hipGetLastError();
+    }
+    logprobs_kernel<T, TOP, true><<<grid_of(f.splits, f.rows), kThreads, 0, stream>>>(f);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (TOP && f.groups > kFewGroups)
+        logprobs_join_kernel<T, TOP, kMaxGroups><<<grid_of(1, f.rows), kThreads, 0, stream>>>(f);
+    else
+        logprobs_join_kernel<T, TOP, kFewGroups><<<grid_of(1, f.rows), kThreads, 0, stream>>>(f);
     return hipGetLastError();
 }
 
@@ -660,7 +771,7 @@ int token_logprobs(const void *logits, const void *targets, int64_t num_rows, in
         return EWG_INVALID_ARGUMENT;
     if (reinterpret_cast<uintptr_t>(logits) % elem) return EWG_INVALID_ARGUMENT;
     const Plan p = plan_for(num_rows, vocab, elem, top_k, compute_units());
-    if (p.splits > 1) {
+    if (p.total > 0) {
         if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return EWG_INVALID_ARGUMENT;
         if (workspace_bytes < p.total) return EWG_WORKSPACE_TOO_SMALL;
     }
@@ -673,22 +784,22 @@ int token_logprobs(const void *logits, const void *targets, int64_t num_rows, in
     f.rows = num_rows;
     f.vocab = (int)vocab;
     f.splits = p.splits;
-    f.groups_per_split = p.groups_per_split;
+    f.loads_per_split = p.loads_per_split;
+    f.groups = p.groups;
     f.top_k = top_k;
     f.inv_t = 1.0f / temperature;
     f.c = kLog2e / temperature;
     f.out = {logprobs, entropy, logsumexp, top_logprobs, top_ids};
-    if (p.splits > 1) {
+    if (p.total > 0) {
         f.stats = reinterpret_cast<Stat *>(ws + p.stats);
-        f.part_values = reinterpret_cast<float *>(ws + p.values);
-        f.part_ids = reinterpret_cast<int *>(ws + p.ids);
+        f.group_max = reinterpret_cast<float *>(ws + p.group_max);
     }
     (void)hipGetLastError();
     hipError_t e;
     if (logits_dtype == EWG_BF16)
-        e = top_k ? launch_forward<BF16, true>(f, stream) : launch_forward<BF16, false>(f, stream);
+        e = top_k ? launch_forward<BF16, true>(f, p.total > 0, stream) : launch_forward<BF16, false>(f, p.total > 0, stream);
     else
-        e = top_k ? launch_forward<F32, true>(f, stream) : launch_forward<F32, false>(f, stream);
+        e = top_k ? launch_forward<F32, true>(f, p.total > 0, stream) : launch_forward<F32, false>(f, p.total > 0, stream);
     return e == hipSuccess ? EWG_OK : EWG_HIP_ERROR;
 }
 
