@@ -10,6 +10,25 @@
 
 #include "ewg_internal.h"
 
+namespace ewg {
+
+int num_cus() {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0) dev = 0;
+    if (dev < 64) {
+        int v = cache[dev].load(std::memory_order_relaxed);
+        if (v > 0) return v;
+    }
+    int v = 0;
+    if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0)
+        v = 256;
+    if (dev < 64) cache[dev].store(v, std::memory_order_relaxed);
+    return v;
+}
+
+}  // namespace ewg
+
 namespace {
 
 using namespace ewg;
@@ -33,22 +52,6 @@ size_t float_size(int d) { return d == EWG_BF16 ? 2 : 4; }
 
 bool aligned(const void *p, int64_t row_stride_bytes, size_t a) {
     return (reinterpret_cast<uintptr_t>(p) % a == 0) && (row_stride_bytes % (int64_t)a == 0);
-}
-
-// Compute units of the current device, cached per device ordinal.
-int num_cus() {
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) dev = 0;
-    if (dev < 64) {
-        int v = cache[dev].load(std::memory_order_relaxed);
-        if (v > 0) return v;
-    }
-    int v = 0;
-    if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0)
-        v = 256;
-    if (dev < 64) cache[dev].store(v, std::memory_order_relaxed);
-    return v;
 }
 
 int check_common(int64_t num_tokens, int64_t hidden, int64_t num_embeddings, int ids_dtype,

@@ -70,6 +70,9 @@ struct SortTables {
     int32_t *chunk_first;
 };
 
+// Compute units of the current device, cached per device ordinal (api.hip).
+int num_cus();
+
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 constexpr int kMaxGrid = 4095;       // workgroups of one launch, at most

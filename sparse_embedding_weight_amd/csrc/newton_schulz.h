@@ -20,7 +20,6 @@ struct NsShape {
     int tall;              // rows > cols: X is its transpose
     int k, len;            // X: min and max of rows, cols
     int kp, lp;            // padded
-    int tile;              // tile side of the products
 };
 
 // Byte offsets in the workspace (one matrix after another inside each part).

@@ -212,7 +212,7 @@ struct NsProduct {
     const _Float16 *p, *q;     // C = P Q^T, both [rows][depth]
     int64_t p_batch, q_batch;
     int depth;                 // padded, a multiple of 64
-    int tiles_p, tiles_q;      // of one matrix
+    int tiles_p;               // along P
     // epilogue
     float factor;              // on the 32-bit sums
     const _Float16 *gram;      // for B: A without its diagonal
@@ -336,7 +336,7 @@ constexpr int kSteps = kDepth / 16;
 // to arrive: with a ring of two the small tile took 43 us where it takes 28
 // with four (k 1024, depth 4096), although two workgroups then share a unit.
 template <int FP>
-constexpr int kStages = FP == 4 ? 2 : 4;
+constexpr int kStages = FP == 4 ? 2 : FP == 2 ? 4 : 8;
 
 // One tile of C = P Q^T, 64 FP x 64 FQ, by four waves of 32 FP x 32 FQ each, kept
 // in registers as 32x32 blocks. P and Q go through a ring of LDS stages of 64
@@ -438,10 +438,56 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
         }
     };
     // a stage's loads go out over three steps; the fourth leaves the last of them time
+    const int kp = a.sh.kp, lp = a.sh.lp;
+    float *diag_a = a.diag_a + (int64_t)batch * kp, *diag_b = a.diag_b + (int64_t)batch * kp;
+    const int64_t base = (int64_t)batch * kp * (SYM ? kp : lp);
+    const int width = SYM ? kp : lp;
+    // What the results are made of: A's halves for B, the state for X. Blocks past
+    // the matrix (its sides are multiples of 64) are left out.
+    using In = typename std::conditional<EPI == kPoly, half4, float4>::type;
+    constexpr bool READS = EPI != kGram;
+    constexpr int EARLY = FP <= 2 ? FP : 0, HELD = FP <= 2 ? FP : 2;    // rows of blocks loaded ahead, held
+    In in[HELD][FQ][4];
+    auto row_of = [&](int i) { return ti * TP + (wp * FP + i) * 32 + r32; };
+    auto block_in = [&](int i, int j) { return ti * TP + (wp * FP + i) * 32 < kp && tj * TQ + (wq * FQ + j) * 32 < width; };
+    auto col_of = [&](int j, int g) { return tj * TQ + (wq * FQ + j) * 32 + g * 8 + h * 4; };
+    // B: A's diagonal of the tile's columns
+    __shared__ float of_cols[EPI == kPoly ? TQ : 1];
+    if constexpr (EPI == kPoly) {
+        for (int c = threadIdx.x; c < TQ; c += 256) of_cols[c] = tj * TQ + c < kp ? diag_a[tj * TQ + c] : 0.0f;
+    }
+    auto fetch = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < FQ; ++j)
+            if (block_in(i, j)) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int64_t at = base + (int64_t)row_of(i) * width + col_of(j, g);
+                    if constexpr (EPI == kPoly) in[i % HELD][j][g] = *reinterpret_cast<const half4 *>(a.gram + at);
+                    if constexpr (EPI == kState || EPI == kLast) in[i % HELD][j][g] = *reinterpret_cast<const float4 *>(a.x + at);
+                }
+            }
+    };
     constexpr int FIRST = LOADS * 3 / 8, SECOND = LOADS * 6 / 8;
 #pragma unroll
     for (int t = 0; t < RING - 1; ++t) stage(t, 0, LOADS);
     stage(RING - 1, 0, FIRST);
+    // What the results are made of is asked for now where registers hold it; these
+    // loads are younger than the first stage's, so the counted waits stay on the safe side.
+    if constexpr (READS) {
+#pragma unroll
+        for (int i = 0; i < EARLY; ++i) fetch(i);
+    }
+    float of_rows[FP];
+#pragma unroll
+    for (int i = 0; i < FP; ++i) {
+        // a + e for X's row; A's diagonal for B's
+        of_rows[i] = 0.0f;
+        if (row_of(i) < kp) {
+            if constexpr (EPI == kPoly) of_rows[i] = diag_a[row_of(i)];
+            if constexpr (EPI == kState || EPI == kLast) of_rows[i] = a.a_coef + diag_b[row_of(i)];
+        }
+    }
     wait_loads<(RING - 2) * LOADS + FIRST>();
     __builtin_amdgcn_s_barrier();
 #pragma unroll
@@ -459,46 +505,16 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
     }
     wait_loads<0>();
 
-    const int kp = a.sh.kp, lp = a.sh.lp;
-    float *diag_a = a.diag_a + (int64_t)batch * kp, *diag_b = a.diag_b + (int64_t)batch * kp;
-    const int64_t base = (int64_t)batch * kp * (SYM ? kp : lp);
-    const int width = SYM ? kp : lp;
-    // What the results are made of (A's halves for B, the state for X): the
-    // loads of one row of blocks go out before the row before is worked on.
-    // Blocks past the matrix (its sides are multiples of 64) are left out.
-    using In = typename std::conditional<EPI == kPoly, half4, float4>::type;
-    constexpr bool READS = EPI != kGram;
-    In in[2][FQ][4];
-    auto row_of = [&](int i) { return ti * TP + (wp * FP + i) * 32 + r32; };
-    auto block_in = [&](int i, int j) { return ti * TP + (wp * FP + i) * 32 < kp && tj * TQ + (wq * FQ + j) * 32 < width; };
-    auto col_of = [&](int j, int g) { return tj * TQ + (wq * FQ + j) * 32 + g * 8 + h * 4; };
-    auto fetch = [&](int i) {
-#pragma unroll
-        for (int j = 0; j < FQ; ++j)
-            if (block_in(i, j)) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int64_t at = base + (int64_t)row_of(i) * width + col_of(j, g);
-                    if constexpr (EPI == kPoly) in[i & 1][j][g] = *reinterpret_cast<const half4 *>(a.gram + at);
-                    if constexpr (EPI == kState || EPI == kLast) in[i & 1][j][g] = *reinterpret_cast<const float4 *>(a.x + at);
-                }
-            }
-    };
-    if constexpr (READS) fetch(0);
+    if constexpr (READS && EARLY == 0) fetch(0);
 #pragma unroll
     for (int i = 0; i < FP; ++i) {
-        // one row of blocks after another: more loads at the front would spill
+        // the next row's loads go out before this one is worked on; more would spill
         asm volatile("" ::: "memory");
         if constexpr (READS)
-            if (i + 1 < FP) fetch(i + 1);
+            if (i + 1 < FP && i + 1 >= EARLY) fetch(i + 1);
         __builtin_amdgcn_sched_barrier(0);
         const int row = row_of(i);
-        // a + e for X's row; A's diagonal for B's
-        float of_row = 0.0f;
-        if (row < kp) {
-            if constexpr (EPI == kPoly) of_row = diag_a[row];
-            if constexpr (EPI == kState || EPI == kLast) of_row = a.a_coef + diag_b[row];
-        }
+        const float of_row = of_rows[i];
 #pragma unroll
         for (int j = 0; j < FQ; ++j) {
             if (!block_in(i, j)) continue;
@@ -511,14 +527,14 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
                 for (int e = 0; e < 4; ++e) v[e] = acc[i][j][g * 4 + e] * a.factor;
                 if constexpr (SYM) {
                     if constexpr (EPI == kPoly) {
-                        const float4 of_col = *reinterpret_cast<const float4 *>(diag_a + col);
+                        const float4 of_col = *reinterpret_cast<const float4 *>(of_cols + col - tj * TQ);
                         const float dc[4] = {of_col.x, of_col.y, of_col.z, of_col.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             if (row == col + e)
                                 diag_b[row] = (v[e] + of_row * __builtin_fmaf(of_row, a.c_coef / kGramScale, a.b_coef)) / kGramScale;
                             v[e] = __builtin_fmaf(__builtin_fmaf(of_row + dc[e], a.c_coef / kGramScale, a.b_coef),
-                                                  (float)in[i & 1][j][g][e], v[e]);
+                                                  (float)in[i % HELD][j][g][e], v[e]);
                         }
                     } else {
 #pragma unroll
@@ -532,7 +548,7 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
                     if (ti != tj)
                         *reinterpret_cast<half4 *>(a.out + base + (int64_t)(col + (lane & 3)) * kp + (row & ~3)) = transpose_quad(o);
                 } else {
-                    const In old = in[i & 1][j][g];
+                    const In old = in[i % HELD][j][g];
                     v[0] = __builtin_fmaf(of_row, old.x, v[0]);
                     v[1] = __builtin_fmaf(of_row, old.y, v[1]);
                     v[2] = __builtin_fmaf(of_row, old.z, v[2]);
@@ -710,17 +726,49 @@ __global__ __launch_bounds__(1024) void ns_small_kernel(NsSource src, NsSink sin
 
 int round_to(int64_t v, int t) { return (int)((v + t - 1) / t * t); }
 
-template <int F, int EPI, class S = BF16, bool WEIGHT = false>
-hipError_t launch_product(const NsProduct &a, const NsSink &sink, hipStream_t stream) {
-    const int tiles = EPI == kGram || EPI == kPoly ? a.tiles_p * (a.tiles_p + 1) / 2 : a.tiles_p * a.tiles_q;
-    ns_product_kernel<F, F, EPI, S, WEIGHT><<<dim3((unsigned)tiles, a.sh.batch), 256, 0, stream>>>(a, sink);
+int tiles_of(int side, int f) { return (side + 64 * f - 1) / (64 * f); }
+
+// Tiles of 64 F x 64 F: of one matrix, by product.
+int64_t tiles_in(bool symmetric, const NsShape &sh, int f) {
+    const int64_t p = tiles_of(sh.kp, f);
+    return symmetric ? p * (p + 1) / 2 : p * tiles_of(sh.lp, f);
+}
+
+// The tile of a product, F = 1, 2 or 4: a small one gives more workgroups where
+// there are few and wastes less of the last round, a large one reads less for
+// what it computes. Rounds of one workgroup a compute unit, with the times of a
+// stage and of a tile's start and end as measured: 0.28, 0.55 and 1.6 us a stage,
+// 4, 5 and 10 us a tile. Of k 1024 and depth 4096 the Gram matrix takes 17, 28
+// and 85 us with the three tiles; of k 4096 and depth 7168, 287, 182 and 170.
+int tile_for(bool symmetric, const NsShape &sh, int depth, int cus) {
+    const float stage[3] = {0.28f, 0.55f, 1.6f}, rest[3] = {4.0f, 5.0f, 10.0f};
+    int best = 1;
+    float least = 0.0f;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t tiles = tiles_in(symmetric, sh, 1 << i) * sh.batch;
+        const float time = (float)((tiles + cus - 1) / cus) * ((float)(depth / kDepth) * stage[i] + rest[i]);
+        if (i == 0 || time < least) {
+            least = time;
+            best = 1 << i;
+        }
+    }
+    return best;
+}
+
+template <int F, int EPI, class S, bool WEIGHT>
+hipError_t launch_product(NsProduct a, const NsSink &sink, hipStream_t stream) {
+    constexpr bool SYM = EPI == kGram || EPI == kPoly;
+    a.tiles_p = tiles_of(a.sh.kp, F);
+    ns_product_kernel<F, F, EPI, S, WEIGHT><<<dim3((unsigned)tiles_in(SYM, a.sh, F), a.sh.batch), 256, 0, stream>>>(a, sink);
     return hipGetLastError();
 }
 
 template <int EPI, class S = BF16, bool WEIGHT = false>
-hipError_t launch_tiled(const NsProduct &a, const NsSink &sink, hipStream_t stream) {
-    return a.sh.tile == 256 ? launch_product<4, EPI, S, WEIGHT>(a, sink, stream)
-                            : launch_product<2, EPI, S, WEIGHT>(a, sink, stream);
+hipError_t launch_tiled(const NsProduct &a, const NsSink &sink, int cus, hipStream_t stream) {
+    const int f = tile_for(EPI == kGram || EPI == kPoly, a.sh, a.depth, cus);
+    return f == 4   ? launch_product<4, EPI, S, WEIGHT>(a, sink, stream)
+           : f == 2 ? launch_product<2, EPI, S, WEIGHT>(a, sink, stream)
+                    : launch_product<1, EPI, S, WEIGHT>(a, sink, stream);
 }
 
 template <class G, bool MOM>
@@ -774,6 +822,7 @@ hipError_t run(const NsSource &src, bool g_bf16, const NsSink &sink, bool out_bf
                           : (mom ? launch_prepare<F32, true>(src, sh, l, ws, eps, x_scale, stream)
                                  : launch_prepare<F32, false>(src, sh, l, ws, eps, x_scale, stream));
     if (e != hipSuccess) return e;
+    const int cus = num_cus();
     _Float16 *xh = reinterpret_cast<_Float16 *>(ws + l.xh);
     _Float16 *xt[2] = {reinterpret_cast<_Float16 *>(ws + l.xt0), reinterpret_cast<_Float16 *>(ws + l.xt1)};
     _Float16 *am = reinterpret_cast<_Float16 *>(ws + l.a), *bm = reinterpret_cast<_Float16 *>(ws + l.b);
@@ -781,8 +830,6 @@ hipError_t run(const NsSource &src, bool g_bf16, const NsSink &sink, bool out_bf
     for (int s = 0; s < steps; ++s) {
         NsProduct a = {};
         a.sh = sh;
-        a.tiles_p = (sh.kp + sh.tile - 1) / sh.tile;
-        a.tiles_q = a.tiles_p;
         a.p = a.q = xh;
         a.p_batch = a.q_batch = kl;
         a.depth = sh.lp;
@@ -790,7 +837,7 @@ hipError_t run(const NsSource &src, bool g_bf16, const NsSink &sink, bool out_bf
         a.diag_b = reinterpret_cast<float *>(ws + l.diag_b);
         a.factor = kGramScale / (x_scale * x_scale);
         a.out = am;
-        if ((e = launch_tiled<kGram>(a, sink, stream)) != hipSuccess) return e;
+        if ((e = launch_tiled<kGram>(a, sink, cus, stream)) != hipSuccess) return e;
         a.p = a.q = am;
         a.p_batch = a.q_batch = kk;
         a.depth = sh.kp;
@@ -799,12 +846,11 @@ hipError_t run(const NsSource &src, bool g_bf16, const NsSink &sink, bool out_bf
         a.b_coef = coef[1];
         a.c_coef = coef[2];
         a.out = bm;
-        if ((e = launch_tiled<kPoly>(a, sink, stream)) != hipSuccess) return e;
+        if ((e = launch_tiled<kPoly>(a, sink, cus, stream)) != hipSuccess) return e;
         a.p = bm;
         a.q = xt[s & 1];
         a.p_batch = kk;
         a.q_batch = kl;
-        a.tiles_q = (sh.lp + sh.tile - 1) / sh.tile;
         a.factor = 1.0f / (kGramScale * x_scale);
         a.a_coef = coef[0];
         a.x_scale = x_scale;
@@ -812,11 +858,11 @@ hipError_t run(const NsSource &src, bool g_bf16, const NsSink &sink, bool out_bf
         a.out = xh;
         a.out_t = xt[(s + 1) & 1];
         if (s + 1 < steps)
-            e = launch_tiled<kState>(a, sink, stream);
+            e = launch_tiled<kState>(a, sink, cus, stream);
         else if (!sink.weight)
-            e = launch_tiled<kLast, BF16, false>(a, sink, stream);
+            e = launch_tiled<kLast, BF16, false>(a, sink, cus, stream);
         else
-            e = out_bf16 ? launch_tiled<kLast, BF16, true>(a, sink, stream) : launch_tiled<kLast, F32, true>(a, sink, stream);
+            e = out_bf16 ? launch_tiled<kLast, BF16, true>(a, sink, cus, stream) : launch_tiled<kLast, F32, true>(a, sink, cus, stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -860,8 +906,7 @@ NsShape ns_shape(int64_t batch, int64_t rows, int64_t cols) {
     s.tall = rows > cols;
     s.k = (int)(rows < cols ? rows : cols);
     s.len = (int)(rows < cols ? cols : rows);
-    s.tile = s.k >= 2048 ? 256 : 128;
-    s.kp = round_to(s.k, 64);
+            s.kp = round_to(s.k, 64);
     s.lp = round_to(s.len, 64);
     return s;
 }

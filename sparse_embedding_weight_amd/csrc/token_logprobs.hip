@@ -26,8 +26,6 @@
 // Backward, one pass that reads the logits and writes the gradient.
 #include <hip/hip_runtime.h>
 
-#include <atomic>
-
 #include "ewg_device.h"
 #include "ewg_internal.h"
 #include "token_logprobs.h"
@@ -669,17 +667,6 @@ struct Plan {
     size_t stats, group_max, total;
 };
 
-int compute_units() {
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-    int v = cache[dev].load(std::memory_order_relaxed);
-    if (v > 0) return v;
-    if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0) v = 256;
-    cache[dev].store(v, std::memory_order_relaxed);
-    return v;
-}
-
 // One workgroup a row where that fills the chip (two rows a compute unit) and
 // the row's group maxima fit; otherwise parts of one set of loads a wave, or as
 // many sets as keep a row to 256 parts and the chip to about eight parts a unit.
@@ -754,7 +741,7 @@ size_t token_logprobs_workspace_bytes(int64_t num_rows, int64_t vocab, int logit
     if (num_rows < 1 || num_rows > EWG_LOGPROBS_MAX_ROWS || vocab < 1 || vocab > EWG_LOGPROBS_MAX_VOCAB ||
         !is_float(logits_dtype) || top_k < 0 || top_k > EWG_MAX_TOP_LOGPROBS)
         return 0;
-    return plan_for(num_rows, vocab, logits_dtype == EWG_BF16 ? 2 : 4, top_k, compute_units()).total;
+    return plan_for(num_rows, vocab, logits_dtype == EWG_BF16 ? 2 : 4, top_k, num_cus()).total;
 }
 
 int token_logprobs(const void *logits, const void *targets, int64_t num_rows, int64_t vocab,
@@ -770,7 +757,7 @@ int token_logprobs(const void *logits, const void *targets, int64_t num_rows, in
     if (!logits || !targets || !logprobs || !entropy || !logsumexp || (top_k > 0 && (!top_logprobs || !top_ids)))
         return EWG_INVALID_ARGUMENT;
     if (reinterpret_cast<uintptr_t>(logits) % elem) return EWG_INVALID_ARGUMENT;
-    const Plan p = plan_for(num_rows, vocab, elem, top_k, compute_units());
+    const Plan p = plan_for(num_rows, vocab, elem, top_k, num_cus());
     if (p.total > 0) {
         if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return EWG_INVALID_ARGUMENT;
         if (workspace_bytes < p.total) return EWG_WORKSPACE_TOO_SMALL;
