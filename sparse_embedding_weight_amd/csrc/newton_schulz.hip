@@ -331,10 +331,11 @@ __device__ __forceinline__ void wait_loads() {
 constexpr int kDepth = 64;       // of a stage: rows of 128 bytes, whole lines of the L2
 constexpr int kSteps = kDepth / 16;
 
-// Stages of the LDS ring, 128 KiB in all. A stage is 2048 clocks of matrix work
-// for a 256 x 256 tile but 512 for a 128 x 128 one, and loads take about 1900
-// to arrive: with a ring of two the small tile took 43 us where it takes 28
-// with four (k 1024, depth 4096), although two workgroups then share a unit.
+// Stages of an LDS ring of 128 KiB (RING below; half of it where two workgroups
+// share a compute unit). A stage is 2048 clocks of matrix work for a 256 x 256
+// tile, 512 for 128 x 128 and 128 for 64 x 64, and loads take about 1900 to
+// arrive: alone on its unit, the middle tile took 43 us with a ring of two where
+// it takes 28 with four (k 1024, depth 4096).
 template <int FP>
 constexpr int kStages = FP == 4 ? 2 : FP == 2 ? 4 : 8;
 
@@ -346,13 +347,12 @@ constexpr int kStages = FP == 4 ? 2 : FP == 2 ? 4 : 8;
 // from the L2 the small tile's products took half as long again. The matrix
 // instruction takes Q as its first operand: a lane then holds four consecutive
 // columns of one row of C.
-template <int FP, int FQ, int EPI, class S, bool WEIGHT>
+template <int FP, int FQ, int RING, int EPI, class S, bool WEIGHT>
 __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sink) {
     constexpr int TP = 64 * FP, TQ = 64 * FQ;
     constexpr int LOADS = (TP + TQ) / 32;            // 1 KiB (8 rows) loads of a wave and stage
     constexpr int BYTES = (TP + TQ) * 128;
     constexpr bool SYM = EPI == kGram || EPI == kPoly;
-    constexpr int RING = kStages<FP>;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[RING * BYTES];
 
     const int lane = threadIdx.x & 63;
@@ -736,17 +736,23 @@ int64_t tiles_in(bool symmetric, const NsShape &sh, int f) {
 
 // The tile of a product, F = 1, 2 or 4: a small one gives more workgroups where
 // there are few and wastes less of the last round, a large one reads less for
-// what it computes. Rounds of one workgroup a compute unit, with the times of a
-// stage and of a tile's start and end as measured: 0.28, 0.55 and 1.6 us a stage,
-// 4, 5 and 10 us a tile. Of k 1024 and depth 4096 the Gram matrix takes 17, 28
-// and 85 us with the three tiles; of k 4096 and depth 7168, 287, 182 and 170.
+// what it computes. Small tiles that outnumber the compute units share them in
+// pairs, with half the ring each. The time of a round is that of its stages and
+// of a tile's start and end, in us as measured: alone 0.22, 0.43 and 1.6 a stage
+// and 4, 7.3 and 10 a tile; in pairs 0.6 and 1.2, 5.5 and 9. Of k 1024 and depth
+// 4096 the Gram matrix takes 18, 28 and 85 us with the three tiles; of k 4096
+// and depth 7168, 278, 197 and 170; twelve of k 448 and depth 1024, 15, 13 and 33.
 int tile_for(bool symmetric, const NsShape &sh, int depth, int cus) {
-    const float stage[3] = {0.28f, 0.55f, 1.6f}, rest[3] = {4.0f, 5.0f, 10.0f};
+    const float stage[3] = {0.22f, 0.43f, 1.6f}, rest[3] = {4.0f, 7.3f, 10.0f};
+    const float paired_stage[2] = {0.6f, 1.2f}, paired_rest[2] = {5.5f, 9.0f};
     int best = 1;
     float least = 0.0f;
     for (int i = 0; i < 3; ++i) {
         const int64_t tiles = tiles_in(symmetric, sh, 1 << i) * sh.batch;
-        const float time = (float)((tiles + cus - 1) / cus) * ((float)(depth / kDepth) * stage[i] + rest[i]);
+        const bool paired = i < 2 && tiles > cus;
+        const int64_t slots = paired ? 2 * cus : cus;
+        const float time = (float)((tiles + slots - 1) / slots) *
+                           ((float)(depth / kDepth) * (paired ? paired_stage[i] : stage[i]) + (paired ? paired_rest[i] : rest[i]));
         if (i == 0 || time < least) {
             least = time;
             best = 1 << i;
@@ -756,19 +762,23 @@ int tile_for(bool symmetric, const NsShape &sh, int depth, int cus) {
 }
 
 template <int F, int EPI, class S, bool WEIGHT>
-hipError_t launch_product(NsProduct a, const NsSink &sink, hipStream_t stream) {
+hipError_t launch_product(NsProduct a, const NsSink &sink, int cus, hipStream_t stream) {
     constexpr bool SYM = EPI == kGram || EPI == kPoly;
     a.tiles_p = tiles_of(a.sh.kp, F);
-    ns_product_kernel<F, F, EPI, S, WEIGHT><<<dim3((unsigned)tiles_in(SYM, a.sh, F), a.sh.batch), 256, 0, stream>>>(a, sink);
+    const dim3 grid((unsigned)tiles_in(SYM, a.sh, F), a.sh.batch);
+    if (F < 4 && (int64_t)grid.x * grid.y > cus)
+        ns_product_kernel<F, F, kStages<F> / (F < 4 ? 2 : 1), EPI, S, WEIGHT><<<grid, 256, 0, stream>>>(a, sink);
+    else
+        ns_product_kernel<F, F, kStages<F>, EPI, S, WEIGHT><<<grid, 256, 0, stream>>>(a, sink);
     return hipGetLastError();
 }
 
 template <int EPI, class S = BF16, bool WEIGHT = false>
 hipError_t launch_tiled(const NsProduct &a, const NsSink &sink, int cus, hipStream_t stream) {
     const int f = tile_for(EPI == kGram || EPI == kPoly, a.sh, a.depth, cus);
-    return f == 4   ? launch_product<4, EPI, S, WEIGHT>(a, sink, stream)
-           : f == 2 ? launch_product<2, EPI, S, WEIGHT>(a, sink, stream)
-                    : launch_product<1, EPI, S, WEIGHT>(a, sink, stream);
+    return f == 4   ? launch_product<4, EPI, S, WEIGHT>(a, sink, cus, stream)
+           : f == 2 ? launch_product<2, EPI, S, WEIGHT>(a, sink, cus, stream)
+                    : launch_product<1, EPI, S, WEIGHT>(a, sink, cus, stream);
 }
 
 template <class G, bool MOM>
