@@ -1,11 +1,13 @@
 """Binding of include/token_logprobs.h: log probabilities of given tokens, with
 entropy and top alternatives, and their gradient. Argument marshalling only."""
+import contextlib
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
-from ._binding import DTYPE_CODE, EWG_OK, EmbeddingWgradError, _stream_handle, lib
+from ._binding import DTYPE_CODE, EWG_OK, EmbeddingWgradError, lib
 
 MAX_TOP_LOGPROBS = 32             # EWG_MAX_TOP_LOGPROBS
 MAX_ROWS = 1048576                # EWG_LOGPROBS_MAX_ROWS
@@ -28,6 +30,25 @@ class TokenLogprobs(NamedTuple):
     logsumexp: torch.Tensor
     top_logprobs: Optional[torch.Tensor]
     top_ids: Optional[torch.Tensor]
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """The context of a call on `device`. The smallest calls take the GPU about 3 us, so
+    that what a call costs on the host is what its caller waits for: the device is
+    switched only where another one is current."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _stream_handle(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_need(index: int, num_rows: int, vocab: int, code: int, top_k: int) -> int:
+    return lib.token_logprobs_workspace_bytes(num_rows, vocab, code, top_k)
 
 
 def token_logprobs_workspace_bytes(num_rows: int, vocab: int, dtype: torch.dtype, top_k: int = 0) -> int:
@@ -103,24 +124,24 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top_k: int = 0, 
     if not 0 <= top_k <= MAX_TOP_LOGPROBS:
         raise ValueError(f"token_logprobs: top_k must lie within 0..{MAX_TOP_LOGPROBS}")
     device, shape, n, vocab = logits.device, targets.shape, targets.numel(), logits.shape[-1]
-    x, t = _rows(logits), targets.reshape(-1)
+    x, t = _rows(logits), targets if targets.dim() == 1 else targets.reshape(-1)
     if not t.is_contiguous():
         t = t.contiguous()
-    numbers = torch.empty((3, *shape), dtype=torch.float32, device=device)
+    lp = torch.empty(shape, dtype=torch.float32, device=device)
+    entropy, lse = torch.empty_like(lp), torch.empty_like(lp)
     top = torch.empty((*shape, top_k), dtype=torch.float32, device=device) if top_k else None
     ids = torch.empty((*shape, top_k), dtype=torch.int64, device=device) if top_k else None
-    out = TokenLogprobs(numbers[0], numbers[1], numbers[2], top, ids)
+    out = TokenLogprobs(lp, entropy, lse, top, ids)
     if n == 0:
         return out
     code = DTYPE_CODE[logits.dtype]
-    with torch.cuda.device(device):
+    with _on(device):
         stream = _stream_handle(device)
-        need = lib.token_logprobs_workspace_bytes(n, vocab, code, top_k)
+        need = _workspace_need(device.index, n, vocab, code, top_k)
         ws = _workspace(need, device, stream, workspace) if need or workspace is not None else None
-        at = numbers.data_ptr()
         st = lib.token_logprobs(
             x.data_ptr(), t.data_ptr(), n, vocab, x.stride(0), code, DTYPE_CODE[t.dtype], temperature,
-            top_k, at, at + 4 * n, at + 8 * n, top.data_ptr() if top_k else None,
+            top_k, lp.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top.data_ptr() if top_k else None,
             ids.data_ptr() if top_k else None, ws.data_ptr() if ws is not None else None,
             ws.numel() if ws is not None else 0, stream)
     if st != EWG_OK:
@@ -165,15 +186,15 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, logsume
         return out
     x = _rows(logits)
     try:
-        o = out.view(n, vocab)
+        o = out if out.dim() == 2 else out.view(n, vocab)
     except RuntimeError:
         o = None
     if o is None or (o.stride(1) != 1 and vocab > 1) or (n > 1 and o.stride(0) < vocab):
         raise ValueError("token_logprobs_backward: out must be viewable as [rows, vocab] with unit column stride")
-    t = targets.reshape(-1)
+    t = targets if targets.dim() == 1 else targets.reshape(-1)
     if not t.is_contiguous():
         t = t.contiguous()
-    with torch.cuda.device(device):
+    with _on(device):
         st = lib.token_logprobs_backward(
             x.data_ptr(), t.data_ptr(), lse.data_ptr(), entropy.data_ptr() if grad_entropy is not None else None,
             grad_logprobs.data_ptr() if grad_logprobs is not None else None,

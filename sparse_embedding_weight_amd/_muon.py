@@ -5,8 +5,8 @@ import math
 
 import torch
 
-from ._binding import DTYPE_CODE, EWG_OK, EmbeddingWgradError, _stream_handle, lib
-from ._logprobs import _workspace
+from ._binding import DTYPE_CODE, EWG_OK, EmbeddingWgradError, lib
+from ._logprobs import _on, _stream_handle, _workspace
 
 NEWTON_SCHULZ_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 MAX_SIDE = 32768                  # EWG_MUON_MAX_SIDE
@@ -83,7 +83,7 @@ def orthogonalize_update(update: torch.Tensor, steps: int = 5, coefficients=NEWT
     if update.numel() == 0:
         return out
     device = update.device
-    with torch.cuda.device(device):
+    with _on(device):
         stream = _stream_handle(device)
         ws = _workspace(lib.orthogonalize_update_workspace_bytes(batch, rows, cols), device, stream, workspace)
         st = lib.orthogonalize_update(update.data_ptr(), out.data_ptr(), batch, rows, cols, bs, rs, obs, ors,
@@ -134,7 +134,7 @@ def muon_step(weight: torch.Tensor, main_grad: torch.Tensor, momentum: torch.Ten
     if weight.numel() == 0:
         return
     scale = math.sqrt(max(1.0, rows / cols)) if scale is None else float(scale)
-    with torch.cuda.device(device):
+    with _on(device):
         stream = _stream_handle(device)
         ws = _workspace(lib.orthogonalize_update_workspace_bytes(batch, rows, cols), device, stream, workspace)
         st = lib.muon_step(weight.data_ptr(), out_weight.data_ptr(), main_grad.data_ptr(), momentum.data_ptr(),
