@@ -331,13 +331,13 @@ __device__ __forceinline__ void wait_loads() {
 constexpr int kDepth = 64;       // of a stage: rows of 128 bytes, whole lines of the L2
 constexpr int kSteps = kDepth / 16;
 
-// Stages of an LDS ring of 128 KiB (RING below; half of it where two workgroups
+// Stages of an LDS ring of 128 or 144 KiB (RING below; half of it where two workgroups
 // share a compute unit). A stage is 2048 clocks of matrix work for a 256 x 256
-// tile, 512 for 128 x 128 and 128 for 64 x 64, and loads take about 1900 to
+// tile, 1152, 512 and 128 for the smaller ones, and loads take about 1900 to
 // arrive: alone on its unit, the middle tile took 43 us with a ring of two where
 // it takes 28 with four (k 1024, depth 4096).
 template <int FP>
-constexpr int kStages = FP == 4 ? 2 : FP == 2 ? 4 : 8;
+constexpr int kStages = FP == 4 ? 2 : FP == 3 ? 3 : FP == 2 ? 4 : 8;
 
 // One tile of C = P Q^T, 64 FP x 64 FQ, by four waves of 32 FP x 32 FQ each, kept
 // in registers as 32x32 blocks. P and Q go through a ring of LDS stages of 64
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
     auto stage = [&](int t, int first, int last) {
         // past the end the last stage is loaded again, so that the count of loads in flight stays the same
         const int from = (t < stages ? t : stages - 1) * kDepth * 2;
-        const uint32_t to = lds0 + (uint32_t)(t & (RING - 1)) * BYTES;
+        const uint32_t to = lds0 + (uint32_t)(t % RING) * BYTES;
 #pragma unroll
         for (int i = first; i < last; ++i) {
             const bool in_p = i < 2 * FP;
@@ -426,7 +426,7 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
     };
     // Step s: its products, the reads of the step after (stage `next`), loads [first, last) of stage `load`
     auto step = [&](int s, int next, int load, int first, int last) {
-        const uint8_t *tile = lds + (next & (RING - 1)) * BYTES;
+        const uint8_t *tile = lds + next % RING * BYTES;
 #pragma unroll
         for (int i = 0; i < FP; ++i) {
             read(tile, (s + 1) % kSteps, i);
@@ -734,28 +734,32 @@ int64_t tiles_in(bool symmetric, const NsShape &sh, int f) {
     return symmetric ? p * (p + 1) / 2 : p * tiles_of(sh.lp, f);
 }
 
-// The tile of a product, F = 1, 2 or 4: a small one gives more workgroups where
-// there are few and wastes less of the last round, a large one reads less for
-// what it computes. Small tiles that outnumber the compute units share them in
-// pairs, with half the ring each. The time of a round is that of its stages and
-// of a tile's start and end, in us as measured: alone 0.22, 0.43 and 1.6 a stage
-// and 4, 7.3 and 10 a tile; in pairs 0.6 and 1.2, 5.5 and 9. Of k 1024 and depth
-// 4096 the Gram matrix takes 18, 28 and 85 us with the three tiles; of k 4096
-// and depth 7168, 278, 197 and 170; twelve of k 448 and depth 1024, 15, 13 and 33.
+// The tile of a product, F = 1 to 4: a small one gives more workgroups where there
+// are few and wastes less of the last round, a large one reads less for what it
+// computes. Tiles of F <= 2 that outnumber the compute units share them in pairs,
+// with half the ring each. A round takes its stages and a tile's start and end,
+// with the times below in us, as measured; the symmetric products end sooner
+// than those that read and write the state. Of k 1024 and depth 4096 the Gram
+// matrix takes 18, 28 and 85 us with F = 1, 2, 4; of k 4096 and depth 7168, 278,
+// 197, 144 and 177 with 1 to 4, where one round of 253 tiles beats one of 136 larger
+// ones; the last product of 7168 x 7168 takes 860 us with 3 and 907 with 4,
+// of 4096 x 7168 406 and 321; of twelve 448 x 1024, 34, 28 and 46 with 1, 2, 4.
 int tile_for(bool symmetric, const NsShape &sh, int depth, int cus) {
-    const float stage[3] = {0.22f, 0.43f, 1.6f}, rest[3] = {4.0f, 7.3f, 10.0f};
-    const float paired_stage[2] = {0.6f, 1.2f}, paired_rest[2] = {5.5f, 9.0f};
+    static const float stage[4] = {0.22f, 0.43f, 1.1f, 1.6f}, paired_stage[2] = {0.6f, 1.2f};
+    static const float rest[2][4] = {{6.0f, 17.0f, 22.0f, 45.0f}, {4.0f, 7.3f, 9.0f, 10.0f}};
+    static const float paired_rest[2][2] = {{6.0f, 20.0f}, {5.5f, 9.0f}};
     int best = 1;
     float least = 0.0f;
-    for (int i = 0; i < 3; ++i) {
-        const int64_t tiles = tiles_in(symmetric, sh, 1 << i) * sh.batch;
-        const bool paired = i < 2 && tiles > cus;
+    for (int f = 1; f <= 4; ++f) {
+        const int64_t tiles = tiles_in(symmetric, sh, f) * sh.batch;
+        const bool paired = f <= 2 && tiles > cus;
         const int64_t slots = paired ? 2 * cus : cus;
-        const float time = (float)((tiles + slots - 1) / slots) *
-                           ((float)(depth / kDepth) * (paired ? paired_stage[i] : stage[i]) + (paired ? paired_rest[i] : rest[i]));
-        if (i == 0 || time < least) {
+        const float a_stage = paired ? paired_stage[f - 1] : stage[f - 1];
+        const float a_tile = paired ? paired_rest[symmetric][f - 1] : rest[symmetric][f - 1];
+        const float time = (float)((tiles + slots - 1) / slots) * ((float)(depth / kDepth) * a_stage + a_tile);
+        if (f == 1 || time < least) {
             least = time;
-            best = 1 << i;
+            best = f;
         }
     }
     return best;
@@ -766,10 +770,13 @@ hipError_t launch_product(NsProduct a, const NsSink &sink, int cus, hipStream_t 
     constexpr bool SYM = EPI == kGram || EPI == kPoly;
     a.tiles_p = tiles_of(a.sh.kp, F);
     const dim3 grid((unsigned)tiles_in(SYM, a.sh, F), a.sh.batch);
-    if (F < 4 && (int64_t)grid.x * grid.y > cus)
-        ns_product_kernel<F, F, kStages<F> / (F < 4 ? 2 : 1), EPI, S, WEIGHT><<<grid, 256, 0, stream>>>(a, sink);
-    else
-        ns_product_kernel<F, F, kStages<F>, EPI, S, WEIGHT><<<grid, 256, 0, stream>>>(a, sink);
+    if constexpr (F <= 2) {
+        if ((int64_t)grid.x * grid.y > cus) {
+            ns_product_kernel<F, F, kStages<F> / 2, EPI, S, WEIGHT><<<grid, 256, 0, stream>>>(a, sink);
+            return hipGetLastError();
+        }
+    }
+    ns_product_kernel<F, F, kStages<F>, EPI, S, WEIGHT><<<grid, 256, 0, stream>>>(a, sink);
     return hipGetLastError();
 }
 
@@ -777,6 +784,7 @@ template <int EPI, class S = BF16, bool WEIGHT = false>
 hipError_t launch_tiled(const NsProduct &a, const NsSink &sink, int cus, hipStream_t stream) {
     const int f = tile_for(EPI == kGram || EPI == kPoly, a.sh, a.depth, cus);
     return f == 4   ? launch_product<4, EPI, S, WEIGHT>(a, sink, cus, stream)
+           : f == 3 ? launch_product<3, EPI, S, WEIGHT>(a, sink, cus, stream)
            : f == 2 ? launch_product<2, EPI, S, WEIGHT>(a, sink, cus, stream)
                     : launch_product<1, EPI, S, WEIGHT>(a, sink, cus, stream);
 }
