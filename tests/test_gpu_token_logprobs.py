@@ -162,6 +162,27 @@ def test_ties_go_to_the_lowest_index(dtype, rows):
     check(x[:2].contiguous(), t[:2], 32)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [1, 3, 700])
+def test_many_large_logits_in_few_places(dtype, rows):
+    """More candidates than are ranked at once: thousands of distinct large logits in a
+    tenth of the lanes or of the groups, and thousands equal to the last one wanted."""
+    vocab, size = 40000, 8 if dtype == torch.bfloat16 else 4               # elements of a 16-byte piece
+    g = torch.Generator().manual_seed(rows)
+    x = torch.randn(rows, vocab, generator=g)
+    at = torch.arange(vocab)
+    large = 50 + torch.randperm(vocab, generator=g).float() / 16
+    x[0] = torch.where((at // size) % 64 < 6, large, x[0])                  # six lanes of every wave load
+    if rows > 1:
+        x[1] = torch.where((at // (16 * size)) % 64 < 6, large, x[1])       # six groups of every 64
+        x[2] = -1e4                                                         # fewer allowed than wanted, a finite mask
+        x[2, ::5000] = 3.0
+    x = x.to(dtype).cuda()
+    t = torch.randint(0, vocab, (rows,), generator=g).cuda()
+    for k in (1, 20, 32):
+        check(x[: min(rows, 3)].contiguous() if k < 20 else x, t[: min(rows, 3)] if k < 20 else t, k)
+
+
 def test_splits_do_not_change_the_alternatives_and_calls_repeat():
     x, t = make(1, 129280, torch.bfloat16, 5)
     many = x.expand(2048, -1).contiguous()
