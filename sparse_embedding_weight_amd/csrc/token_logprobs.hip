@@ -60,6 +60,34 @@ struct Stat {
     float m, s, w;
 };
 
+typedef uint32_t word4 __attribute__((ext_vector_type(4)));
+
+// A 16-byte piece (or one element, E = 1); ONCE: past the caches, which larger
+// tensors would only flush.
+template <bool ONCE, class V, int E>
+__device__ __forceinline__ void load_stream(const V *p, V (&v)[E]) {
+    if constexpr (!ONCE) {
+        load_vec<V, E>(p, v);
+    } else if constexpr (E == 1) {
+        v[0] = __builtin_nontemporal_load(p);
+    } else {
+        const word4 w = __builtin_nontemporal_load(reinterpret_cast<const word4 *>(p));
+        __builtin_memcpy(v, &w, 16);
+    }
+}
+template <bool ONCE, class V, int E>
+__device__ __forceinline__ void store_stream(V *p, const V (&v)[E]) {
+    if constexpr (!ONCE) {
+        store_vec<V, E>(p, v);
+    } else if constexpr (E == 1) {
+        __builtin_nontemporal_store(v[0], p);
+    } else {
+        word4 w;
+        __builtin_memcpy(&w, v, 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<word4 *>(p));
+    }
+}
+
 template <class T>
 constexpr int kPiece = 16 / (int)sizeof(typename T::T);    // elements of a 16-byte piece
 
@@ -417,7 +445,7 @@ __device__ __forceinline__ void write_row(const Forward &f, int64_t row, Stat t,
 
 // One part of a row, or the whole of it (PARTS false). A wave load is 64 pieces;
 // a wave takes sets of kUnroll loads in turn with the others.
-template <class T, bool TOP, bool PARTS>
+template <class T, bool TOP, bool PARTS, bool ONCE>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(Forward f) {
     constexpr int E = kPiece<T>;
     using V = typename T::T;
@@ -449,7 +477,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(Forward f) {
             // inside the row, the same for the whole wave: the loads go out back to back
             V raw[kUnroll][E];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) load_vec<V, E>(x + from + (u * 64 + lane) * E, raw[u]);
+            for (int u = 0; u < kUnroll; ++u) load_stream<ONCE>(x + from + (u * 64 + lane) * E, raw[u]);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
@@ -581,7 +609,7 @@ constexpr int kBackUnroll = 4;         // pieces a lane has in flight
 // for the gradients g of the log probability and h of the entropy H. PIECES:
 // logits and gradient rows share their offset in 16 bytes; otherwise one
 // element at a time.
-template <class T, bool PIECES>
+template <class T, bool PIECES, bool ONCE>
 __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(Backward f) {
     constexpr int E = PIECES ? kPiece<T> : 1;
     using V = typename T::T;
@@ -627,14 +655,14 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(Backward f)
         // inside the row, the same for the whole workgroup
         V raw[kBackUnroll][E];
 #pragma unroll
-        for (int u = 0; u < kBackUnroll; ++u) load_vec<V, E>(x + from + (u * kThreads + (int)threadIdx.x) * E, raw[u]);
+        for (int u = 0; u < kBackUnroll; ++u) load_stream<ONCE>(x + from + (u * kThreads + (int)threadIdx.x) * E, raw[u]);
 #pragma unroll
         for (int u = 0; u < kBackUnroll; ++u) {
             float v[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) v[e] = T::widen(raw[u][e]);
             grad_piece(v, q0 + u * kThreads + threadIdx.x, raw[u]);
-            store_vec<V, E>(out + from + (u * kThreads + (int)threadIdx.x) * E, raw[u]);
+            store_stream<ONCE>(out + from + (u * kThreads + (int)threadIdx.x) * E, raw[u]);
         }
         return;
     }
@@ -705,13 +733,27 @@ int check_sizes(int64_t rows, int64_t vocab, int64_t stride, int logits_dtype, i
     return EWG_OK;
 }
 
+// Whether logits of this size are read past the caches, as the gradient is
+// written: from half of the 256 MiB last-level cache on. The gradient of 8192 x
+// 129280 bf16 takes 688 us so and 780 through the caches (either side alone:
+// 794, 758), of 2047 x 32003 fp32 78 and 97; the forward pass of the former 318
+// and 360. Smaller ones stay, for the kernel that reads them next. With
+// alternatives the few groups read again are wanted in the caches.
+bool past_caches(int64_t bytes) { return bytes >= (int64_t)128 << 20; }
+
 template <class T, bool TOP>
 hipError_t launch_forward(const Forward &f, bool parts, hipStream_t stream) {
     if (!parts) {
-        logprobs_kernel<T, TOP, false><<<grid_of(1, f.rows), kThreads, 0, stream>>>(f);
+        if constexpr (!TOP) {
+            if (past_caches(f.rows * f.vocab * (int64_t)sizeof(typename T::T))) {
+                logprobs_kernel<T, TOP, false, true><<<grid_of(1, f.rows), kThreads, 0, stream>>>(f);
+                return hipGetLastError();
+            }
+        }
+        logprobs_kernel<T, TOP, false, false><<<grid_of(1, f.rows), kThreads, 0, stream>>>(f);
         return hipGetLastError();
     }
-    logprobs_kernel<T, TOP, true><<<grid_of(f.splits, f.rows), kThreads, 0, stream>>>(f);
+    logprobs_kernel<T, TOP, true, false><<<grid_of(f.splits, f.rows), kThreads, 0, stream>>>(f);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (TOP && f.groups > kFewGroups)
@@ -724,10 +766,12 @@ hipError_t launch_forward(const Forward &f, bool parts, hipStream_t stream) {
 template <class T>
 hipError_t launch_backward(const Backward &f, bool pieces, hipStream_t stream) {
     const dim3 grid = grid_of(f.chunks, f.rows);
-    if (pieces)
-        logprobs_backward_kernel<T, true><<<grid, kThreads, 0, stream>>>(f);
+    if (!pieces)
+        logprobs_backward_kernel<T, false, false><<<grid, kThreads, 0, stream>>>(f);
+    else if (past_caches(f.rows * f.vocab * (int64_t)sizeof(typename T::T)))
+        logprobs_backward_kernel<T, true, true><<<grid, kThreads, 0, stream>>>(f);
     else
-        logprobs_backward_kernel<T, false><<<grid, kThreads, 0, stream>>>(f);
+        logprobs_backward_kernel<T, true, false><<<grid, kThreads, 0, stream>>>(f);
     return hipGetLastError();
 }
 
