@@ -446,7 +446,8 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
     // the matrix (its sides are multiples of 64) are left out.
     using In = typename std::conditional<EPI == kPoly, half4, float4>::type;
     constexpr bool READS = EPI != kGram;
-    constexpr int EARLY = FP <= 2 ? FP : 0, HELD = FP <= 2 ? FP : 2;    // rows of blocks loaded ahead, held
+    // (all rows ahead rather than one at a time: 807 us instead of 860 for 7168 x 7168)
+    constexpr int EARLY = FP <= 3 ? FP : 0, HELD = FP <= 3 ? FP : 2;    // rows of blocks loaded ahead, held
     In in[HELD][FQ][4];
     auto row_of = [&](int i) { return ti * TP + (wp * FP + i) * 32 + r32; };
     auto block_in = [&](int i, int j) { return ti * TP + (wp * FP + i) * 32 < kp && tj * TQ + (wq * FQ + j) * 32 < width; };
@@ -742,11 +743,11 @@ int64_t tiles_in(bool symmetric, const NsShape &sh, int f) {
 // than those that read and write the state. Of k 1024 and depth 4096 the Gram
 // matrix takes 18, 28 and 85 us with F = 1, 2, 4; of k 4096 and depth 7168, 278,
 // 197, 144 and 177 with 1 to 4, where one round of 253 tiles beats one of 136 larger
-// ones; the last product of 7168 x 7168 takes 860 us with 3 and 907 with 4,
+// ones; the last product of 7168 x 7168 takes 807 us with 3 and 907 with 4,
 // of 4096 x 7168 406 and 321; of twelve 448 x 1024, 34, 28 and 46 with 1, 2, 4.
 int tile_for(bool symmetric, const NsShape &sh, int depth, int cus) {
     static const float stage[4] = {0.22f, 0.43f, 1.1f, 1.6f}, paired_stage[2] = {0.6f, 1.2f};
-    static const float rest[2][4] = {{6.0f, 17.0f, 22.0f, 45.0f}, {4.0f, 7.3f, 9.0f, 10.0f}};
+    static const float rest[2][4] = {{6.0f, 17.0f, 14.0f, 45.0f}, {4.0f, 7.3f, 9.0f, 10.0f}};
     static const float paired_rest[2][2] = {{6.0f, 20.0f}, {5.5f, 9.0f}};
     int best = 1;
     float least = 0.0f;
