@@ -75,7 +75,9 @@ __device__ __forceinline__ float load_u(const NsSource &s, int b, int r, int c) 
 // a fixed share and a fixed order for every workgroup. One pass over main_grad
 // and momentum, bound by HBM: four elements of a row at a time, four of those
 // in flight a lane; a lane's next place is its last plus a constant number of
-// rows and columns, so that no index is divided in the loop.
+// rows and columns, so that no index is divided in the loop (with a 64-bit
+// division an element it took 479 us for 7168 x 7168 with momentum; now 107, 617
+// MB at 5.8 TB/s).
 template <class G, bool MOM>
 __global__ __launch_bounds__(256) void ns_norm_kernel(NsSource s, int rows, int cols, int vector,
                                                       double *__restrict__ partials) {
@@ -154,6 +156,8 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(NsSource s, int rows, int 
 
 // ---- 2. X = u / (|u| + eps) in its three layouts ----------------------------
 
+// One 64 x 64 tile a workgroup, turned in LDS so that every layout is read and
+// written in whole lines. Bound by HBM: 822 MB of 7168 x 7168 in 195 us (4.2 TB/s).
 template <class G, bool MOM>
 __global__ __launch_bounds__(256) void ns_layout_kernel(NsSource s, NsShape sh, int parts, float eps,
                                                         float x_scale,
@@ -212,7 +216,7 @@ struct NsProduct {
     const _Float16 *p, *q;     // C = P Q^T, both [rows][depth]
     int64_t p_batch, q_batch;
     int depth;                 // padded, a multiple of 64
-    int tiles_p;               // along P
+    int tiles_p, tiles_q;      // of one matrix
     // epilogue
     float factor;              // on the 32-bit sums
     const _Float16 *gram;      // for B: A without its diagonal
@@ -339,6 +343,50 @@ constexpr int kSteps = kDepth / 16;
 template <int FP>
 constexpr int kStages = FP == 4 ? 2 : FP == 3 ? 3 : FP == 2 ? 4 : 8;
 
+// The tile of workgroup b. Workgroups go to the eight dies (XCDs) in turn, each
+// with an L2 of its own: a die takes a run of tiles that follow each other, and
+// they follow each other down bands of eight tile rows, so that the 32 tiles
+// that run on a die share 8 + 4 panels of P and Q (in plain order 19 + 7 of a
+// 38 x 38 grid). Reads past the L2 fall to 55 %; that takes 3 % off the symmetric
+// products of 7168 x 7168, and 17 % off the last one of twelve 1023 x 389.
+constexpr int kDies = 8, kBand = 8;
+
+template <bool SYM>
+__device__ __forceinline__ void tile_of(int b, int tiles_p, int tiles_q, int batches, int &batch, int &ti, int &tj) {
+    const int per = SYM ? tiles_p * (tiles_p + 1) / 2 : tiles_p * tiles_q;
+    const int total = per * batches;
+    const int die = b % kDies, each = total / kDies, more = total % kDies;
+    int n = die * each + (die < more ? die : more) + b / kDies;
+    batch = uniform(n / per);
+    n -= batch * per;
+    if constexpr (SYM) {
+        // the row of tile n of the lower triangle taken row by row gives its band
+        int r = (int)((sqrtf(8.0f * (float)n + 1.0f) - 1.0f) * 0.5f);
+        while ((r + 1) * (r + 2) / 2 <= n) ++r;
+        while (r * (r + 1) / 2 > n) --r;
+        const int r0 = uniform(r / kBand * kBand);
+        const int rows = tiles_p - r0 < kBand ? tiles_p - r0 : kBand;
+        n -= r0 * (r0 + 1) / 2;
+        if (n < r0 * rows) {
+            tj = uniform(n / rows);
+            ti = r0 + n - tj * rows;
+        } else {
+            // the band's end on the diagonal, column by column
+            n -= r0 * rows;
+            tj = 0;
+            while (n >= rows - tj) n -= rows - tj++;
+            ti = r0 + tj + n;
+            tj += r0;
+        }
+    } else {
+        const int r0 = uniform(n / (kBand * tiles_q)) * kBand;
+        const int rows = tiles_p - r0 < kBand ? tiles_p - r0 : kBand;
+        n -= r0 * tiles_q;
+        tj = uniform(n / rows);
+        ti = r0 + n - tj * rows;
+    }
+}
+
 // One tile of C = P Q^T, 64 FP x 64 FQ, by four waves of 32 FP x 32 FQ each, kept
 // in registers as 32x32 blocks. P and Q go through a ring of LDS stages of 64
 // halves of depth; a wave reads the operands of the next 16 of depth from LDS
@@ -358,20 +406,8 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int stages = a.depth / kDepth;
-    const int batch = blockIdx.y;
-    int ti, tj;
-    if constexpr (SYM) {
-        // blocks count the tiles of the lower triangle row by row
-        const int n = blockIdx.x;
-        ti = (int)((sqrtf(8.0f * (float)n + 1.0f) - 1.0f) * 0.5f);
-        while ((ti + 1) * (ti + 2) / 2 <= n) ++ti;
-        while (ti * (ti + 1) / 2 > n) --ti;
-        ti = uniform(ti);
-        tj = n - ti * (ti + 1) / 2;
-    } else {
-        tj = uniform((int)blockIdx.x / a.tiles_p);
-        ti = (int)blockIdx.x - tj * a.tiles_p;
-    }
+    int batch, ti, tj;
+    tile_of<SYM>((int)blockIdx.x, a.tiles_p, a.tiles_q, a.sh.batch, batch, ti, tj);
 
     // Buffer descriptors of the tile's rows of P and Q: base, bytes, raw format. A
     // tile is at most 256 rows of 64 KiB, so offsets fit; rows of the last tile that
@@ -575,9 +611,10 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
 // Up to 128 x 128 everything lives in one workgroup: 16 waves of one 32x32 block
 // each, the state in their registers, the half copies of X, its transpose, A
 // and B in LDS (128 KiB). A launch for each product costs more than the
-// products: 17 launches took 120 us for one 128 x 128 matrix, this takes the
-// time of one launch and some 20 us of dependent LDS reads and barriers. A
-// batch is one workgroup a matrix.
+// products: 17 launches took 120 us for one 128 x 128 matrix, this takes 34: 12
+// for the start, the norm and the end, and 4.4 a step, of which the vector work
+// on 16 values a lane after each of three products is the largest part. A batch
+// is one workgroup a matrix (256 of 128 x 128: 45 us).
 constexpr int kSmall = 128;
 
 // half (row, col) of a 128 x 128 LDS matrix, 16-byte pieces swizzled as above
@@ -747,7 +784,7 @@ int64_t tiles_in(bool symmetric, const NsShape &sh, int f) {
 // of 4096 x 7168 406 and 321; of twelve 448 x 1024, 34, 28 and 46 with 1, 2, 4.
 int tile_for(bool symmetric, const NsShape &sh, int depth, int cus) {
     static const float stage[4] = {0.22f, 0.43f, 1.1f, 1.6f}, paired_stage[2] = {0.6f, 1.2f};
-    static const float rest[2][4] = {{6.0f, 17.0f, 14.0f, 45.0f}, {4.0f, 7.3f, 9.0f, 10.0f}};
+    static const float rest[2][4] = {{6.0f, 17.0f, 22.0f, 45.0f}, {4.0f, 7.3f, 9.0f, 10.0f}};
     static const float paired_rest[2][2] = {{6.0f, 20.0f}, {5.5f, 9.0f}};
     int best = 1;
     float least = 0.0f;
@@ -770,9 +807,12 @@ template <int F, int EPI, class S, bool WEIGHT>
 hipError_t launch_product(NsProduct a, const NsSink &sink, int cus, hipStream_t stream) {
     constexpr bool SYM = EPI == kGram || EPI == kPoly;
     a.tiles_p = tiles_of(a.sh.kp, F);
-    const dim3 grid((unsigned)tiles_in(SYM, a.sh, F), a.sh.batch);
+    a.tiles_q = SYM ? a.tiles_p : tiles_of(a.sh.lp, F);
+    const int64_t tiles = tiles_in(SYM, a.sh, F) * a.sh.batch;
+    if (tiles > (1 << 23)) return hipErrorInvalidValue;      // more than a grid, or the card's memory, holds
+    const unsigned grid = (unsigned)tiles;
     if constexpr (F <= 2) {
-        if ((int64_t)grid.x * grid.y > cus) {
+        if (tiles > cus) {
             ns_product_kernel<F, F, kStages<F> / 2, EPI, S, WEIGHT><<<grid, 256, 0, stream>>>(a, sink);
             return hipGetLastError();
         }

@@ -23,7 +23,14 @@
 // the parts leave their states and group maxima in the workspace, and a second
 // kernel, one workgroup a row, joins them and finds the alternatives once.
 //
-// Backward, one pass that reads the logits and writes the gradient.
+// What bounds it: 8192 x 129280 bf16 is read in 320 us, 6.6 TB/s (a large copy
+// reaches 4.9 TB/s of reads and writes); the vector units are busy for most of
+// that (11 instructions and an exponential a logit). Alternatives cost a short
+// row most: 2047 x 32003 bf16 with 8 takes 38 us, 3.5 TB/s. 48 x 129280 fp32 with
+// 20 takes 7 us for the parts and 11 for the join, whose steps wait on each other.
+//
+// Backward, one pass that reads the logits and writes the gradient: 8192 x 129280
+// bf16 in 690 us, 6.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "ewg_device.h"
