@@ -611,8 +611,8 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
 // Up to 128 x 128 everything lives in one workgroup: 16 waves of one 32x32 block
 // each, the state in their registers, the half copies of X, its transpose, A
 // and B in LDS (128 KiB). A launch for each product costs more than the
-// products: 17 launches took 120 us for one 128 x 128 matrix, this takes 34: 12
-// for the start, the norm and the end, and 4.4 a step, of which the vector work
+// products: 17 launches took 120 us for one 128 x 128 matrix, this takes 32: 12
+// for the start, the norm and the end, and 4 a step, of which the vector work
 // on 16 values a lane after each of three products is the largest part. A batch
 // is one workgroup a matrix (256 of 128 x 128: 45 us).
 constexpr int kSmall = 128;
@@ -632,7 +632,10 @@ __global__ __launch_bounds__(1024) void ns_small_kernel(NsSource src, NsSink sin
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int batch = blockIdx.x;
-    const int wi = wave >> 2, wj = wave & 3;
+    // Block (wi, wj) of a wave, four bits each: the ten of the lower triangle, all that
+    // the symmetric products compute, spread over the four SIMDs (wave % 4) as 3, 3, 2, 2.
+    const int block = (int)(0xb76321cfed98a540ull >> (4 * wave)) & 15;
+    const int wi = block >> 2, wj = block & 3;
     const int r32 = lane & 31, h = lane >> 5;
     const int row = wi * 32 + r32;
     const int col0 = wj * 32 + h * 4;            // value 4 g + e of a lane: column col0 + 8 g + e

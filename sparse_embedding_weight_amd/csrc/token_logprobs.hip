@@ -26,7 +26,7 @@
 // What bounds it: 8192 x 129280 bf16 is read in 320 us, 6.6 TB/s (a large copy
 // reaches 4.9 TB/s of reads and writes); the vector units are busy for most of
 // that (11 instructions and an exponential a logit). Alternatives cost a short
-// row most: 2047 x 32003 bf16 with 8 takes 38 us, 3.5 TB/s. 48 x 129280 fp32 with
+// row most: 2047 x 32003 bf16 with 8 takes 35 us, 3.7 TB/s. 48 x 129280 fp32 with
 // 20 takes 7 us for the parts and 11 for the join, whose steps wait on each other.
 //
 // Backward, one pass that reads the logits and writes the gradient: 8192 x 129280
@@ -260,18 +260,24 @@ __device__ __forceinline__ void collect(TopScratch<GROUPS> &t, const typename T:
     constexpr int E = kPiece<T>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int listed = t.listed;
-    for (int j = wave * kWaveGroups; j < listed; j += kWaves * kWaveGroups) {
-        float v[E];
-        const int first = load_listed<T>(row, lead, vocab, t.list, j, listed, v);
+    constexpr int AHEAD = 2;           // sets of four groups in flight
+    for (int j = wave * kWaveGroups; j < listed; j += AHEAD * kWaves * kWaveGroups) {
+        float v[AHEAD][E];
+        int first[AHEAD];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (v[e] > bound || (EQUAL && v[e] == bound && v[e] > kNegInf)) {
-                const int at = atomicAdd(&t.count, 1);
-                if (at < kCandidates) {
-                    t.value[at] = v[e];
-                    t.index[at] = first + e;
+        for (int u = 0; u < AHEAD; ++u)
+            first[u] = load_listed<T>(row, lead, vocab, t.list, j + u * kWaves * kWaveGroups, listed, v[u]);
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (v[u][e] > bound || (EQUAL && v[u][e] == bound && v[u][e] > kNegInf)) {
+                    const int at = atomicAdd(&t.count, 1);
+                    if (at < kCandidates) {
+                        t.value[at] = v[u][e];
+                        t.index[at] = first[u] + e;
+                    }
                 }
-            }
     }
 }
 
@@ -292,15 +298,18 @@ __device__ __forceinline__ void top_of_row(TopScratch<GROUPS> &t, const typename
     float m = t.lane_max[lane];
 #pragma unroll
     for (int i = 1; i < kWaves; ++i) m = max2(m, t.lane_max[i * 64 + lane]);
-    int above = 0, reach = 0;
+    // Bit by bit from the top, on integers in the order of the values: a lane's compare
+    // and a scalar count a bit, where ranking 64 lanes takes 300 vector instructions.
+    const int bits = __float_as_int(m == 0.0f ? 0.0f : m);
+    const uint32_t key = (uint32_t)(bits >= 0 ? bits : bits ^ 0x7fffffff) ^ 0x80000000u;
+    uint32_t kth = 0;
 #pragma unroll
-    for (int j = 0; j < 64; ++j) {
-        const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(m), j));
-        above += w > m;
-        reach += w >= m;
+    for (int b = 31; b >= 0; --b) {
+        const uint32_t next = kth | 1u << b;
+        if (__popcll(__ballot(key >= next)) >= k) kth = next;
     }
-    const uint64_t who = __ballot(above < k && k <= reach);
-    const float bound = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(m), who ? __ffsll((unsigned long long)who) - 1 : 0));
+    const int back = (int)(kth ^ 0x80000000u);
+    const float bound = __int_as_float(back >= 0 ? back : back ^ 0x7fffffff);
     auto reaches = [&](int g) {
         const float v = g < n ? t.group_max[g] : kNegInf;
         return v >= bound && v > kNegInf;
@@ -579,10 +588,16 @@ __global__ __launch_bounds__(kThreads) void logprobs_join_kernel(Forward f) {
     if constexpr (TOP) {
         const int n = (lead + f.vocab + 64 * kPiece<T> - 1) / (64 * kPiece<T>) * kWaveGroups;
         float m = kNegInf;
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const float g = f.group_max[row * f.groups + i];
-            scratch.group_max[i] = g;
-            m = max2(m, g);
+        constexpr int AHEAD = 8;       // loads in flight: one after another they took most of the kernel
+        for (int base = threadIdx.x; base < n; base += AHEAD * kThreads) {
+            float g[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) g[u] = base + u * kThreads < n ? f.group_max[row * f.groups + base + u * kThreads] : kNegInf;
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                if (base + u * kThreads < n) scratch.group_max[base + u * kThreads] = g[u];
+                m = max2(m, g[u]);
+            }
         }
         scratch.lane_max[threadIdx.x] = m;
         __syncthreads();
