@@ -71,6 +71,16 @@ __device__ __forceinline__ float load_u(const NsSource &s, int b, int r, int c) 
     return s.nesterov ? __builtin_fmaf(s.beta, m, g) : m;
 }
 
+// The sum over a workgroup of 256, in a fixed order, in every lane.
+__device__ __forceinline__ double workgroup_sum(double v) {
+    __shared__ double of_wave[4];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+    if ((threadIdx.x & 63) == 0) of_wave[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return of_wave[0] + of_wave[1] + of_wave[2] + of_wave[3];
+}
+
 // Sums u^2 in 64 bits (squares of 1e-25 or 1e25 neither vanish nor overflow),
 // a fixed share and a fixed order for every workgroup. One pass over main_grad
 // and momentum, bound by HBM: four elements of a row at a time, four of those
@@ -136,22 +146,32 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(NsSource s, int rows, int 
         }
     } else {
         while (r < rows) {
-            const int64_t at = b * s.m_batch + r * s.m_row + c;
-            float m = 0.0f;
-            if constexpr (MOM) m = s.m[at];
-            one(G::widen(g0[r * s.g_row + c]), m, m);
-            if constexpr (MOM) s.m_out[at] = m;
-            advance();
+            constexpr int AHEAD = 8;
+            typename G::T g[AHEAD];
+            float m[AHEAD];
+            int64_t at[AHEAD];
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (r < rows) {
+                    g[i] = g0[r * s.g_row + c];
+                    if constexpr (MOM) {
+                        at[i] = b * s.m_batch + r * s.m_row + c;
+                        m[i] = s.m[at[i]];
+                    }
+                    n = i + 1;
+                    advance();
+                }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (i < n) {
+                    one(G::widen(g[i]), m[i], m[i]);
+                    if constexpr (MOM) s.m_out[at[i]] = m[i];
+                }
         }
     }
-    __shared__ double part[256];
-    part[threadIdx.x] = sum;
-    __syncthreads();
-    for (int n = 128; n > 0; n >>= 1) {
-        if ((int)threadIdx.x < n) part[threadIdx.x] += part[threadIdx.x + n];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) partials[(int64_t)b * kNsMaxPartials + blockIdx.x] = part[0];
+    sum = workgroup_sum(sum);
+    if (threadIdx.x == 0) partials[(int64_t)b * kNsMaxPartials + blockIdx.x] = sum;
 }
 
 // ---- 2. X = u / (|u| + eps) in its three layouts ----------------------------
@@ -166,38 +186,47 @@ __global__ __launch_bounds__(256) void ns_layout_kernel(NsSource s, NsShape sh, 
                                                         _Float16 *__restrict__ xh,
                                                         _Float16 *__restrict__ xt) {
     __shared__ float t[64][65];
-    __shared__ double part[256];
     const int b = blockIdx.z, tid = threadIdx.x;
-    double share = 0.0;
-    for (int i = tid; i < parts; i += 256) share += partials[(int64_t)b * kNsMaxPartials + i];
-    part[tid] = share;
-    __syncthreads();
-    for (int n = 128; n > 0; n >>= 1) {
-        if (tid < n) part[tid] += part[tid + n];
-        __syncthreads();
-    }
-    // Division by the norm in 64 bits: 1 / norm need not fit 32 bits for tiny updates.
-    const double inverse = 1.0 / (sqrt(part[0]) + (double)eps);
     const int i0 = blockIdx.x * 64, j0 = blockIdx.y * 64;   // X tile: rows i0.., columns j0..
     const int lane = tid & 63, w = tid >> 6;
-    for (int q = w; q < 64; q += 4) {
-        // one source row of the tile: X row i0+q, or X column j0+q of a tall update
-        const int r = (sh.tall ? j0 : i0) + q, c = (sh.tall ? i0 : j0) + lane;
-        float v = 0.0f;
-        if (r < sh.rows && c < sh.cols) v = (float)((double)load_u<G, MOM>(s, b, r, c) * inverse);
+    // source rows of the tile (X's rows, or its columns where the update is tall), all
+    // sixteen of a wave in flight
+    float u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = (sh.tall ? j0 : i0) + i * 4 + w, c = (sh.tall ? i0 : j0) + lane;
+        u[i] = r < sh.rows && c < sh.cols ? load_u<G, MOM>(s, b, r, c) : 0.0f;
+    }
+    double sum = 0.0;
+    for (int i = tid; i < parts; i += 256) sum += partials[(int64_t)b * kNsMaxPartials + i];
+    sum = workgroup_sum(sum);
+    // Division by the norm in 64 bits: 1 / norm need not fit 32 bits for tiny updates.
+    const double inverse = 1.0 / (sqrt(sum) + (double)eps);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float v = (float)((double)u[i] * inverse);
         if (sh.tall)
-            t[lane][q] = v;
+            t[lane][i * 4 + w] = v;
         else
-            t[q][lane] = v;
+            t[i * 4 + w][lane] = v;
     }
     __syncthreads();
     const int64_t base = (int64_t)b * sh.kp * sh.lp;
-    for (int q = w; q < 64; q += 4) {
-        const int64_t at = base + (int64_t)(i0 + q) * sh.lp + j0 + lane;
-        const float v = t[q][lane];
-        x[at] = v;
-        xh[at] = (_Float16)(v * x_scale);
-        xt[base + (int64_t)(j0 + q) * sh.kp + i0 + lane] = (_Float16)(t[lane][q] * x_scale);
+    // four columns a lane, four rows a wave
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int q = i * 16 + w * 4 + (lane >> 4), c = (lane & 15) * 4;
+        const int64_t at = base + (int64_t)(i0 + q) * sh.lp + j0 + c;
+        const float v[4] = {t[q][c], t[q][c + 1], t[q][c + 2], t[q][c + 3]};
+        half4 o, ot;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            o[e] = (_Float16)(v[e] * x_scale);
+            ot[e] = (_Float16)(t[c + e][q] * x_scale);
+        }
+        *reinterpret_cast<float4 *>(x + at) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<half4 *>(xh + at) = o;
+        *reinterpret_cast<half4 *>(xt + base + (int64_t)(j0 + q) * sh.kp + i0 + c) = ot;
     }
 }
 
@@ -330,6 +359,14 @@ __device__ __forceinline__ void load_to_lds(int4v base, int voffset, int soffset
 template <int N>
 __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+
+// A barrier that no LDS access is moved across. (The LDS of a stage is read by
+// other waves than the one that waited for its loads.)
+__device__ __forceinline__ void stage_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 constexpr int kDepth = 64;       // of a stage: rows of 128 bytes, whole lines of the L2
@@ -526,7 +563,7 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
         }
     }
     wait_loads<(RING - 2) * LOADS + FIRST>();
-    __builtin_amdgcn_s_barrier();
+    stage_barrier();
 #pragma unroll
     for (int i = 0; i < FP; ++i) read(lds, 0, i);
     for (int t = 0; t < stages; ++t) {
@@ -537,7 +574,7 @@ __global__ __launch_bounds__(256) void ns_product_kernel(NsProduct a, NsSink sin
         // stage t + 1 is there for every wave, and every wave has read all of stage t
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         wait_loads<(RING - 2) * LOADS>();
-        __builtin_amdgcn_s_barrier();
+        stage_barrier();
         step(3, t + 1, t + RING, 0, FIRST);
     }
     wait_loads<0>();
