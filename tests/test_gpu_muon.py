@@ -65,6 +65,31 @@ def test_orthogonalize_large(shape):
     assert off(ewg.orthogonalize_update(u), want) < TOL + BF16
 
 
+@pytest.mark.parametrize("shape", [(40, 200, 260), (300, 170, 150), (3, 1300, 1500), (2500, 2700), (2700, 2500), (4096, 1024),
+                                   (8, 700, 900), (64, 310, 300), (2, 2304, 2304), (100, 256, 512), (6530, 6600)])
+def test_every_tile_size(shape):
+    """Sizes and batches for which the products take each of their tiles, alone and in
+    pairs, with partly filled last tiles; the reference in 64 bits on the GPU."""
+    u = make(shape, torch.bfloat16, 21, rank=20)
+
+    def on_gpu(x):
+        if x.shape[-2] > x.shape[-1]:
+            return on_gpu(x.transpose(-2, -1).contiguous()).transpose(-2, -1)
+        x = x / (x.flatten(-2).norm(dim=-1)[..., None, None] + 1e-7)
+        a, b, c = ewg.NEWTON_SCHULZ_COEFFICIENTS
+        for _ in range(5):
+            y = x @ x.transpose(-2, -1).contiguous()
+            x = a * x + (b * y + c * (y @ y)) @ x
+        return x
+
+    want = on_gpu(u.double()).cpu()
+    assert off(ewg.orthogonalize_update(u), want) < TOL + BF16
+    w, m = torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+    ewg.muon_step(w, u, m, lr=1.0, beta=0.5, nesterov=False, scale=1.0)      # weight = -result, in 32 bits
+    assert off(-w, want) < TOL
+    assert torch.equal(m, u.float())
+
+
 @pytest.mark.parametrize("rank", [1, 4, 30])
 def test_orthogonalize_strong_directions_over_noise(rank):
     u = make((240, 300), torch.float32, rank, rank=rank)
