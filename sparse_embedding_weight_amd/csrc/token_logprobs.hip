@@ -27,7 +27,7 @@
 // reaches 4.9 TB/s of reads and writes); the vector units are busy for most of
 // that (11 instructions and an exponential a logit). Alternatives cost a short
 // row most: 2047 x 32003 bf16 with 8 takes 35 us, 3.7 TB/s. 48 x 129280 fp32 with
-// 20 takes 7 us for the parts and 11 for the join, whose steps wait on each other.
+// 20 takes 7 us for the parts and 10 for the join, whose steps wait on each other.
 //
 // Backward, one pass that reads the logits and writes the gradient: 8192 x 129280
 // bf16 in 690 us, 6.1 TB/s.
