@@ -12,11 +12,11 @@
 //
 // For the alternatives the pass keeps nothing per element: only the maximum of
 // each group of sixteen 16-byte pieces (256 bytes), which costs four DPP steps
-// a wave load. Of these maxima, dealt to the 256 lanes of a workgroup, the
-// top_k-th largest lane's is a lower bound on the top_k-th largest element, and
-// a close one (a few lanes hold two of the largest); only the groups that reach
-// it are read again, and the two or three dozen elements above it are ranked
-// against each other. Elements equal to it are taken in index order.
+// a wave load. Of the elements dealt to 64 lanes, the top_k-th largest lane's
+// maximum is a lower bound on the top_k-th largest element, and a close one (a
+// few lanes hold two of the largest); only the groups that reach it are read
+// again, and the two or three dozen elements that do are ranked against each
+// other. Where more than 256 do, those equal to it are taken in index order.
 //
 // A row is one workgroup's where there are many, so that nothing but the
 // results is written. Few rows are cut into parts of one set of loads a wave;
@@ -27,11 +27,13 @@
 // reaches 4.9 TB/s of reads and writes); the vector units are busy for most of
 // that (11 instructions and an exponential a logit). Alternatives cost a short
 // row most: 2047 x 32003 bf16 with 8 takes 35 us, 3.7 TB/s. 48 x 129280 fp32 with
-// 20 takes 7 us for the parts and 10 for the join, whose steps wait on each other.
+// 20 takes 7 us for the parts and 9 for the join, whose steps wait on each other.
 //
 // Backward, one pass that reads the logits and writes the gradient: 8192 x 129280
 // bf16 in 690 us, 6.1 TB/s.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "ewg_device.h"
 #include "ewg_internal.h"
@@ -231,6 +233,7 @@ struct TopScratch {
     int index[kCandidates];
     float best[kMaxTopK];
     int best_at[kMaxTopK];
+    float bound;
     int listed, count;
 };
 
@@ -292,34 +295,42 @@ __device__ __forceinline__ void top_of_row(TopScratch<GROUPS> &t, const typename
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     value = kNegInf;
     index = -1;
-    // The bound, in every wave: the k-th largest of 64 maxima of a quarter-lane's
-    // each. (Of all 256 it would be little closer: of 20 wanted, 24 elements reach
-    // this one.)
-    float m = t.lane_max[lane];
+    if (wave == 0) {
+        // The bound: the k-th largest of 64 maxima of four lanes' each. (Of all 256 it
+        // would be little closer: of 20 wanted, 24 elements reach this one.) Bit by bit
+        // from the top, on integers in the order of the values: a lane's compare and a
+        // scalar count a bit, where ranking 64 lanes takes 300 vector instructions. One
+        // wave does it: the scalar unit is the whole compute unit's.
+        float m = t.lane_max[lane];
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) m = max2(m, t.lane_max[i * 64 + lane]);
-    // Bit by bit from the top, on integers in the order of the values: a lane's compare
-    // and a scalar count a bit, where ranking 64 lanes takes 300 vector instructions.
-    const int bits = __float_as_int(m == 0.0f ? 0.0f : m);
-    const uint32_t key = (uint32_t)(bits >= 0 ? bits : bits ^ 0x7fffffff) ^ 0x80000000u;
-    uint32_t kth = 0;
+        for (int i = 1; i < kWaves; ++i) m = max2(m, t.lane_max[i * 64 + lane]);
+        const int bits = __float_as_int(m == 0.0f ? 0.0f : m);
+        const uint32_t key = (uint32_t)(bits >= 0 ? bits : bits ^ 0x7fffffff) ^ 0x80000000u;
+        // the low half of a bfloat16 value is zero: of its key all zeros, or all ones below zero
+        constexpr int LOWEST = std::is_same<T, BF16>::value ? 16 : 0;
+        uint32_t kth = 0;
 #pragma unroll
-    for (int b = 31; b >= 0; --b) {
-        const uint32_t next = kth | 1u << b;
-        if (__popcll(__ballot(key >= next)) >= k) kth = next;
+        for (int b = 31; b >= LOWEST; --b) {
+            const uint32_t next = kth | 1u << b;
+            if (__popcll(__ballot(key >= next)) >= k) kth = next;
+        }
+        if (LOWEST && !(kth >> 31)) kth |= 0xffffu;
+        const int back = (int)(kth ^ 0x80000000u);
+        if (lane == 0) {
+            t.bound = __int_as_float(back >= 0 ? back : back ^ 0x7fffffff);
+            t.listed = t.count = 0;
+        }
+        if (lane < kMaxTopK) {
+            t.best[lane] = kNegInf;
+            t.best_at[lane] = -1;
+        }
     }
-    const int back = (int)(kth ^ 0x80000000u);
-    const float bound = __int_as_float(back >= 0 ? back : back ^ 0x7fffffff);
+    __syncthreads();
+    const float bound = t.bound;
     auto reaches = [&](int g) {
         const float v = g < n ? t.group_max[g] : kNegInf;
         return v >= bound && v > kNegInf;
     };
-    if (threadIdx.x == 0) t.listed = t.count = 0;
-    if (threadIdx.x < kMaxTopK) {
-        t.best[threadIdx.x] = kNegInf;
-        t.best_at[threadIdx.x] = -1;
-    }
-    __syncthreads();
     for (int base = wave * 64; base < n; base += kThreads) {
         const bool on = reaches(base + lane);
         const uint64_t hits = __ballot(on);
