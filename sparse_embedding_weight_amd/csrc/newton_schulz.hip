@@ -349,7 +349,8 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // to the LDS bytes [lds, lds + 1024). Written as an instruction because the
 // compiler, which cannot tell the stages of the ring apart, would wait for all
 // loads in flight before every LDS read. It has no output register; what has
-// arrived is settled by wait_loads and a barrier before a stage is read.
+// arrived is settled by wait_loads and a barrier before a stage is read. m0 is
+// reserved: the compiler keeps nothing in it.
 __device__ __forceinline__ void load_to_lds(int4v base, int voffset, int soffset, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :: "s"(lds), "v"(voffset), "s"(base), "s"(soffset) : "memory");
